@@ -316,9 +316,9 @@ def _run_own(st):
         g = st["g"] if st["fmt"] == "nv" else None
         if op == "quantize":
             if g is not None:
-                moe.moe_fp4_tensor_scale(st["x"], g)
-            moe.moe_quantize_fp4(fmt, st["x"], g, st["codes"], st["scales"])
-        moe.moe_dequantize_fp4(fmt, st["codes"], st["scales"], g, st["values"])
+                moe.moe_tensor_scale_microscaled(st["x"], g)
+            moe.moe_quantize_microscaled(fmt, st["x"], g, st["codes"], st["scales"])
+        moe.moe_dequantize_microscaled(fmt, st["codes"], st["scales"], g, st["values"])
         return (st["values"], g) if (op == "quantize" and g is not None) else st["values"]
     gs, off = st["group_start"], st["offsets"]
     if op == "product":
@@ -328,10 +328,9 @@ def _run_own(st):
         moe.moe_grouped_gemm_dgrad(st["shape_dx"], st["dy"], gs, off, st["w"], st["dx"], st["ws"])
         moe.moe_grouped_gemm_wgrad(st["shape"], st["dy"], st["x"], gs, off, st["dw"], st["ws"])
         return st["dx"], st["dw"]
-    nv = st["fmt"] == "nv"
-    moe.moe_grouped_gemm_fp4(st["shape"], moe.MOE_NVFP4 if nv else moe.MOE_MXFP4, st["xq"], st["xs"],
-                             st["xg"] if nv else None, gs, off, st["wq"], st["wscale"], st["wg"] if nv else None,
-                             st["y"], st["ws"])
+    fmt, xg, wg = (moe.MOE_NVFP4, st["xg"], st["wg"]) if st["fmt"] == "nv" else (moe.MOE_MXFP4, None, None)
+    moe.moe_grouped_gemm_microscaled(st["shape"], fmt, st["xq"], st["xs"], xg, gs, off, st["wq"], st["wscale"], wg,
+                                     st["y"], st["ws"])
     return st["y"]
 
 
