@@ -360,6 +360,111 @@ moe_status moe_forward_expert_choice(const moe_config* cfg, int64_t capacity, co
                                      float* losses, int32_t* sel, float* gates, void* ws, size_t ws_bytes,
                                      cudaStream_t stream);
 
+/* ---- Ragged products grouped by expert, in 16 and in 4 bits.
+ *
+ * Expert e owns count_e = offsets[e+1] - offsets[e] rows, any number, none
+ * included, of a row buffer: from row group_start[e] on, or back to back from row
+ * offsets[e] on when group_start is NULL. moe_dispatch's offsets and group_start
+ * can be passed as they are, and so can groups without padding between them.
+ * Rows of the buffer that no expert owns are neither used nor written. Groups of
+ * one call must not overlap, and a result must not overlap an operand. A group
+ * that does not lie inside the buffer is recorded as a device check failure and
+ * treated as empty.
+ * Unlike moe_expert_gate_up and moe_expert_down, which need groups padded to
+ * MOE_ROW_ALIGN rows and widths that are multiples of 128, these take any group
+ * sizes and any widths n and k that are multiples of 8.
+ * The workspace is moe_grouped_workspace_bytes() bytes, 256-byte aligned, cleared
+ * once with moe_workspace_init; only failures are recorded in it
+ * (moe_get_device_status), so calls on several streams may share one. */
+
+/* Supported: 0 <= rows <= 2^28 (0 launches nothing but moe_grouped_gemm_wgrad's
+ * zeros); 1 <= n_experts <= 256; n and k multiples of 8 in [8, 32768] (k a multiple
+ * of 32 for moe_grouped_gemm_microscaled). out_dtype is the type of the call's
+ * result. Operands are bf16, sums fp32. */
+typedef struct moe_grouped_shape {
+  int64_t rows;      /* rows of the buffers, owned or not */
+  int32_t n_experts;
+  int32_t n;         /* rows of an expert's weight: the product's output width */
+  int32_t k;         /* columns of an expert's weight: the product's input width */
+  int32_t out_dtype; /* moe_dtype */
+} moe_grouped_shape;
+
+size_t moe_grouped_workspace_bytes(void);
+
+/* y[r] = W_e x[r] for every row r of expert e.
+ *   x [device] [rows, k] bf16;  w [device] [n_experts, n, k] bf16
+ *   y [device] [rows, n] out_dtype, rows without an owner left as they were
+ *   group_start [device] [n_experts + 1] int32 or NULL (the last entry is not read)
+ *   offsets     [device] [n_experts + 1] int32 */
+moe_status moe_grouped_gemm(const moe_grouped_shape* shape, const void* x, const int32_t* group_start,
+                            const int32_t* offsets, const void* w, void* y, void* ws, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/* Its gradient with respect to x: dx[r] = W_e^T dy[r].
+ *   dy [device] [rows, n] bf16;  dx [device] [rows, k] out_dtype, rows without an
+ *   owner left as they were; the others as above. */
+moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const void* dy, const int32_t* group_start,
+                                  const int32_t* offsets, const void* w, void* dx, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
+/* Its gradient with respect to w: dW_e = sum over the rows r of e of dy[r] x[r]^T,
+ * zero for an expert without rows; overwritten, not accumulated. The sum over a
+ * group is taken in parts of 512 rows that are added in fp32.
+ *   dw [device] [n_experts, n, k] out_dtype. */
+moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, const void* x,
+                                  const int32_t* group_start, const int32_t* offsets, void* dw, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/* Microscaled 4-bit values. An element is one of 0, .5, 1, 1.5, 2, 3, 4, 6 with a
+ * sign (E2M1, bit 3 the sign), two to a byte, the first in the low nibble; a block
+ * of neighbours in a row shares a scale byte.
+ *   MOE_MXFP4  blocks of 32, scale 2^(byte - 127): 2^(floor(log2 amax) - 2), at
+ *              least 2^-127; byte 255 is NaN. No tensor scale.
+ *   MOE_NVFP4  blocks of 16, scale an E4M3 byte: amax / (6 g) rounded to nearest
+ *              (ties to even, at most 448), g the tensor scale; byte 127 is NaN, bit 7 is zero.
+ * An element is the representable number nearest to x / (scale * g), ties to the
+ * even code, at most 6; both roundings are of the exact quotients. A block that
+ * holds an infinity or a NaN gets the NaN scale and reads back as NaN, and so does
+ * every block under a tensor scale outside [2^-100, 2^117].
+ * Matrices are [groups, rows, cols] with one tensor scale per group (an expert's
+ * weight, or all rows of an activation buffer): groups >= 1, rows >= 0, cols a
+ * multiple of 32 in [32, 2^20], at most 2^40 elements. All pointers but the tensor
+ * scale's are 16-byte aligned. */
+typedef enum moe_microscaled_format { MOE_MXFP4 = 0, MOE_NVFP4 = 1 } moe_microscaled_format;
+
+/* scale[group] = max(amax / 2688, 2^-100), amax over the group's finite elements:
+ * the g that puts the largest block scale at 448.
+ *   x [device] [groups, rows, cols] of `dtype` (moe_dtype);  scale [device] [groups] fp32 out */
+moe_status moe_tensor_scale_microscaled(int64_t groups, int64_t rows, int64_t cols, int32_t dtype, const void* x,
+                                        float* scale, cudaStream_t stream);
+
+/*   x            [device] [groups, rows, cols] of `dtype`
+ *   tensor_scale [device] [groups] fp32, or NULL for 1 (must be NULL for MOE_MXFP4)
+ *   codes        [device] [groups, rows, cols / 2] out
+ *   scales       [device] [groups, rows, cols / 32 or / 16] out */
+moe_status moe_quantize_microscaled(int32_t format, int64_t groups, int64_t rows, int64_t cols, int32_t dtype,
+                                    const void* x, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                                    cudaStream_t stream);
+
+/* out = element * scale * g, rounded once to fp32 (and then to bf16): arguments as
+ * for moe_quantize_microscaled, out [device] [groups, rows, cols] of `dtype`. */
+moe_status moe_dequantize_microscaled(int32_t format, int64_t groups, int64_t rows, int64_t cols, int32_t dtype,
+                                      const uint8_t* codes, const uint8_t* scales, const float* tensor_scale,
+                                      void* out, cudaStream_t stream);
+
+/* moe_grouped_gemm on 4-bit operands of one format:
+ * y[r] = x_scale * w_scale[e] * sum_k (x code * block scale)(w code * block scale).
+ *   x_codes [device] [rows, k / 2], x_scales [device] [rows, k / 32 or / 16],
+ *   x_scale [device] [1] fp32 or NULL for 1
+ *   w_codes [device] [n_experts, n, k / 2], w_scales [device] [n_experts, n, k / 32 or / 16],
+ *   w_scale [device] [n_experts] fp32 or NULL for 1 (both NULL for MOE_MXFP4)
+ *   the others as for moe_grouped_gemm. */
+moe_status moe_grouped_gemm_microscaled(const moe_grouped_shape* shape, int32_t format, const uint8_t* x_codes,
+                                        const uint8_t* x_scales, const float* x_scale, const int32_t* group_start,
+                                        const int32_t* offsets, const uint8_t* w_codes, const uint8_t* w_scales,
+                                        const float* w_scale, void* y, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
 /* Stage timing for profiling. When `events` is non-NULL, the next call of
  * moe_forward records events[0] on its stream before the router and events[i]
  * after stage i (1 router, 2 dispatch, 3 gate/up GEMM, 4 down GEMM, 5 combine;

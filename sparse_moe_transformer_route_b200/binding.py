@@ -22,6 +22,9 @@ MOE_BF16 = 0
 MOE_FP32 = 1
 MOE_ROUTER_SOFTMAX_TOPK = 0
 MOE_ROUTER_RENORM = 1
+MOE_MXFP4 = 0
+MOE_NVFP4 = 1
+MICRO_BLOCK = {MOE_MXFP4: 32, MOE_NVFP4: 16}  # elements that share a scale byte
 ROW_ALIGN = 128
 
 STATUS_NAMES = {
@@ -41,7 +44,9 @@ EXPORTS = (
     "moe_expert_gate_up", "moe_expert_down", "moe_expert_ffn", "moe_combine", "moe_forward",
     "moe_forward_decode", "moe_forward_host", "moe_forward_host_async", "moe_backward", "moe_rmsnorm", "moe_combine_residual",
     "moe_stack_forward", "moe_stack_forward_trace", "moe_expert_choice_capacity", "moe_route_expert_choice",
-    "moe_forward_expert_choice", "moe_set_stage_events", "moe_get_device_status",
+    "moe_forward_expert_choice", "moe_grouped_workspace_bytes", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+    "moe_grouped_gemm_wgrad", "moe_tensor_scale_microscaled", "moe_quantize_microscaled",
+    "moe_dequantize_microscaled", "moe_grouped_gemm_microscaled", "moe_set_stage_events", "moe_get_device_status",
 )
 STAGE_EVENTS = 6
 STAGES = ("router", "dispatch", "gate_up", "down", "combine")
@@ -68,9 +73,22 @@ class moe_config(ctypes.Structure):
     ]
 
 
+class moe_grouped_shape(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("n_experts", ctypes.c_int32),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(moe_config)
+_GSH = ctypes.POINTER(moe_grouped_shape)
+_I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "moe_abi_version": (ctypes.c_int32, []),
@@ -102,6 +120,15 @@ _SIGS = {
                                                ctypes.c_size_t, _P]),
     "moe_forward_expert_choice": (ctypes.c_int, [_CFG, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                                  ctypes.c_size_t, _P]),
+    "moe_grouped_workspace_bytes": (ctypes.c_size_t, []),
+    "moe_grouped_gemm": (ctypes.c_int, [_GSH, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_grouped_gemm_dgrad": (ctypes.c_int, [_GSH, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_grouped_gemm_wgrad": (ctypes.c_int, [_GSH, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_tensor_scale_microscaled": (ctypes.c_int, [_I64, _I64, _I64, _I32, _P, _P, _P]),
+    "moe_quantize_microscaled": (ctypes.c_int, [_I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P]),
+    "moe_dequantize_microscaled": (ctypes.c_int, [_I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P]),
+    "moe_grouped_gemm_microscaled": (ctypes.c_int, [_GSH, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                    ctypes.c_size_t, _P]),
     "moe_set_stage_events": (ctypes.c_int, [_P]),
     "moe_get_device_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
 }
@@ -482,6 +509,164 @@ def moe_stack_forward(cfg, layers, resid, ws, stream=None):
     st = lib().moe_stack_forward(_cfgp(cfg), n, wr, bs, wgu, wd, _ptr(resid, torch.float32, (T, d), "resid"),
                                  _ptr(ws, torch.uint8, name="ws"), ws.numel(), _stream(stream))
     _check(st, "moe_stack_forward")
+
+
+# ---------------------------------------------------------------- ragged products, 4-bit values
+
+
+def _one_device(*tensors):
+    """The tensors lie on the current device, the one the call launches on."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensors must be on the current device (cuda:{cur}), got {t.device}")
+
+
+def grouped_shape(rows, n_experts, n, k, out_dtype=torch.bfloat16):
+    """A moe_grouped_shape: buffers of `rows` rows, weights [n_experts, n, k], and the
+    type of the call's result (torch.bfloat16 or torch.float32)."""
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    return moe_grouped_shape(int(rows), int(n_experts), int(n), int(k),
+                             MOE_BF16 if out_dtype == torch.bfloat16 else MOE_FP32)
+
+
+def moe_grouped_workspace_bytes() -> int:
+    return lib().moe_grouped_workspace_bytes()
+
+
+def grouped_workspace(shape=None, device="cuda"):
+    """Allocate (torch) and initialise a workspace for the ragged products; one serves
+    every shape."""
+    ws = torch.empty(moe_grouped_workspace_bytes(), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws)
+    return ws
+
+
+def _out_dtype(shape):
+    return torch.bfloat16 if shape.out_dtype == MOE_BF16 else torch.float32
+
+
+def _group_ptrs(shape, group_start, offsets):
+    E = shape.n_experts
+    return (_ptr(group_start, torch.int32, (E + 1,), "group_start", allow_none=True),
+            _ptr(offsets, torch.int32, (E + 1,), "offsets"))
+
+
+def moe_grouped_gemm(shape, x, group_start, offsets, w, y, ws, stream=None):
+    """y[r] = W_e x[r] for the rows r of expert e: rows [group_start[e], + count_e), or
+    [offsets[e], offsets[e+1]) when group_start is None."""
+    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
+    gs, off = _group_ptrs(shape, group_start, offsets)
+    px, pw = _ptr(x, torch.bfloat16, (R, k), "x"), _ptr(w, torch.bfloat16, (E, n, k), "w")
+    py = _ptr(y, _out_dtype(shape), (R, n), "y")
+    pws = _ptr(ws, torch.uint8, name="ws")
+    _one_device(x, group_start, offsets, w, y, ws)
+    st = lib().moe_grouped_gemm(ctypes.byref(shape), px, gs, off, pw, py, pws, ws.numel(), _stream(stream))
+    _check(st, "moe_grouped_gemm")
+
+
+def moe_grouped_gemm_dgrad(shape, dy, group_start, offsets, w, dx, ws, stream=None):
+    """dx[r] = W_e^T dy[r]: the gradient of moe_grouped_gemm with respect to x."""
+    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
+    gs, off = _group_ptrs(shape, group_start, offsets)
+    pdy, pw = _ptr(dy, torch.bfloat16, (R, n), "dy"), _ptr(w, torch.bfloat16, (E, n, k), "w")
+    pdx = _ptr(dx, _out_dtype(shape), (R, k), "dx")
+    pws = _ptr(ws, torch.uint8, name="ws")
+    _one_device(dy, group_start, offsets, w, dx, ws)
+    st = lib().moe_grouped_gemm_dgrad(ctypes.byref(shape), pdy, gs, off, pw, pdx, pws, ws.numel(), _stream(stream))
+    _check(st, "moe_grouped_gemm_dgrad")
+
+
+def moe_grouped_gemm_wgrad(shape, dy, x, group_start, offsets, dw, ws, stream=None):
+    """dW_e = sum over the rows r of e of dy[r] x[r]^T (zero without rows)."""
+    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
+    gs, off = _group_ptrs(shape, group_start, offsets)
+    pdy, px = _ptr(dy, torch.bfloat16, (R, n), "dy"), _ptr(x, torch.bfloat16, (R, k), "x")
+    pdw = _ptr(dw, _out_dtype(shape), (E, n, k), "dw")
+    pws = _ptr(ws, torch.uint8, name="ws")
+    _one_device(dy, x, group_start, offsets, dw, ws)
+    st = lib().moe_grouped_gemm_wgrad(ctypes.byref(shape), pdy, px, gs, off, pdw, pws, ws.numel(), _stream(stream))
+    _check(st, "moe_grouped_gemm_wgrad")
+
+
+def _micro_block(fmt):
+    if fmt not in MICRO_BLOCK:
+        raise ValueError("format must be MOE_MXFP4 or MOE_NVFP4")
+    return MICRO_BLOCK[fmt]
+
+
+def _micro_shape(t, name):
+    """[groups, rows, cols] of a matrix or a stack of matrices."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must have two or three dimensions")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _micro_ptrs(fmt, t, name, tensor_scale, codes, scales):
+    """Shape, dtype code and pointers of a conversion between `t` and its 4-bit form."""
+    block = _micro_block(fmt)
+    G, R, K = _micro_shape(t, name)
+    if K % 32:
+        raise ValueError(f"{name} must have a multiple of 32 columns, got {K}")
+    lead = tuple(t.shape[:-1])
+    pt = _ptr(t, None, None, name)
+    pc = _ptr(codes, torch.uint8, (*lead, K // 2), "codes")
+    ps = _ptr(scales, torch.uint8, (*lead, K // block), "scales")
+    pg = _ptr(tensor_scale, torch.float32, (G,), "tensor_scale", allow_none=True)
+    _one_device(t, tensor_scale, codes, scales)
+    return G, R, K, MOE_BF16 if t.dtype == torch.bfloat16 else MOE_FP32, pt, pg, pc, ps
+
+
+def moe_tensor_scale_microscaled(x, scale, stream=None):
+    """scale[g] = max(amax of x[g] / 2688, 2^-100), the tensor scale MOE_NVFP4 blocks are
+    scaled against. x: [groups, rows, cols], or [rows, cols] as one group."""
+    G, R, K = _micro_shape(x, "x")
+    px, pg = _ptr(x, None, None, "x"), _ptr(scale, torch.float32, (G,), "scale")
+    _one_device(x, scale)
+    st = lib().moe_tensor_scale_microscaled(G, R, K, MOE_BF16 if x.dtype == torch.bfloat16 else MOE_FP32, px, pg,
+                                            _stream(stream))
+    _check(st, "moe_tensor_scale_microscaled")
+
+
+def moe_quantize_microscaled(fmt, x, tensor_scale, codes, scales, stream=None):
+    """x [groups, rows, cols] (or [rows, cols]) to 4-bit codes [.., cols / 2] and block
+    scales [.., cols / 32] (MOE_MXFP4) or [.., cols / 16] (MOE_NVFP4), uint8."""
+    G, R, K, dt, px, pg, pc, ps = _micro_ptrs(fmt, x, "x", tensor_scale, codes, scales)
+    st = lib().moe_quantize_microscaled(fmt, G, R, K, dt, px, pg, pc, ps, _stream(stream))
+    _check(st, "moe_quantize_microscaled")
+
+
+def moe_dequantize_microscaled(fmt, codes, scales, tensor_scale, out, stream=None):
+    """The values that codes and scales stand for, into out [groups, rows, cols] (or
+    [rows, cols]), bf16 or fp32."""
+    G, R, K, dt, po, pg, pc, ps = _micro_ptrs(fmt, out, "out", tensor_scale, codes, scales)
+    st = lib().moe_dequantize_microscaled(fmt, G, R, K, dt, pc, ps, pg, po, _stream(stream))
+    _check(st, "moe_dequantize_microscaled")
+
+
+def moe_grouped_gemm_microscaled(shape, fmt, x_codes, x_scales, x_scale, group_start, offsets, w_codes, w_scales,
+                                 w_scale, y, ws, stream=None):
+    """moe_grouped_gemm on 4-bit rows and weights of one format; x_scale [1] and
+    w_scale [n_experts] are the tensor scales of MOE_NVFP4 operands (None: 1)."""
+    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
+    block = _micro_block(fmt)
+    gs, off = _group_ptrs(shape, group_start, offsets)
+    pxc, pxs = _ptr(x_codes, torch.uint8, (R, k // 2), "x_codes"), _ptr(x_scales, torch.uint8, (R, k // block), "x_scales")
+    pwc = _ptr(w_codes, torch.uint8, (E, n, k // 2), "w_codes")
+    pws_ = _ptr(w_scales, torch.uint8, (E, n, k // block), "w_scales")
+    pxg = _ptr(x_scale, torch.float32, (1,), "x_scale", allow_none=True)
+    pwg = _ptr(w_scale, torch.float32, (E,), "w_scale", allow_none=True)
+    py = _ptr(y, _out_dtype(shape), (R, n), "y")
+    pws = _ptr(ws, torch.uint8, name="ws")
+    _one_device(x_codes, x_scales, x_scale, group_start, offsets, w_codes, w_scales, w_scale, y, ws)
+    st = lib().moe_grouped_gemm_microscaled(ctypes.byref(shape), fmt, pxc, pxs, pxg, gs, off, pwc, pws_, pwg, py, pws,
+                                            ws.numel(), _stream(stream))
+    _check(st, "moe_grouped_gemm_microscaled")
 
 
 def moe_set_stage_events(events):

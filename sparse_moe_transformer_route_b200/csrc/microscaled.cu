@@ -1,0 +1,374 @@
+// Microscaled 4-bit floating point: a tensor's scale, quantisation and the way back.
+//
+// An element holds one of 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign (E2M1) and a block
+// of elements shares a scale:
+//   MXFP4  32 elements, scale s = 2^(floor(log2 amax) - 2), at least 2^-127, held as
+//          its biased exponent (E8M0);
+//   NVFP4  16 elements, scale s = amax / (6 g) rounded to E4M3 (nearest, ties to
+//          even, at most 448), g the fp32 scale of the whole tensor (1 when absent).
+// The element is the representable number nearest to x / (s g), ties to the even
+// code, saturating at 6. Both roundings are those of the real quotients, not of
+// an fp32 approximation of them, so the codes do not depend on how they are
+// computed. A block that holds an infinity or a NaN gets the NaN scale and zero
+// codes, and so reads back as NaN.
+//
+// All three kernels are bound by memory: quantisation reads 2 (bf16) or 4 (fp32)
+// bytes an element and writes 1/2 + 1/16 (NVFP4) or 1/2 + 1/32 (MXFP4); the way
+// back is the reverse. A thread takes 32 bytes of the wide side, two 16-byte
+// accesses, so a warp covers 1 KB of it without gaps; a block's threads (1 to 4)
+// find amax with shuffles.
+#include "moe_internal.h"
+#include "sm100.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kMinTensorScale = 0x1p-100f;
+constexpr float kMaxTensorScale = 0x1p117f;  // within both, 1 / (6 g) and 1 / (s g) are normal; amax / 2688 is below it
+
+template <typename T>
+constexpr int elems_per_thread() {
+  return 32 / static_cast<int>(sizeof(T));
+}
+
+// 32 bytes of input as fp32 values.
+template <typename T>
+__device__ __forceinline__ void load_row32(const T* src, float (&v)[elems_per_thread<T>()]) {
+  const uint4* s4 = reinterpret_cast<const uint4*>(src);
+  const uint4 a = __ldg(s4), b = __ldg(s4 + 1);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      const float2 f = bf16x2_to_float2(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// Eight values to eight E2M1 codes, the first in the lowest nibble (nearest, ties
+// to the even code, saturating).
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n\t"
+      "mov.b32 %0, {t0, t1, t2, t3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Two values to E4M3 (nearest even, saturating): `lo` in the low byte.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The value of a non-negative E4M3 byte other than NaN.
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+  const uint32_t e = b >> 3, m = b & 7u;
+  return e == 0 ? static_cast<float>(m) * 0x1p-9f : __uint_as_float(((e + 120u) << 23) | (m << 20));
+}
+
+// The magnitude that E2M1 code m (0..7) stands for: fields at the top of an fp32's
+// exponent and mantissa give the value times 2^-126, m = 1 as a subnormal.
+__device__ __forceinline__ float e2m1_value(uint32_t m) { return __uint_as_float(m << 22) * 0x1p126f; }
+
+// fp32 approximations of a quotient are off by less than 2^-22 of it, so when the
+// quotient times 1 - 2^-20 and times 1 + 2^-20 round alike, that is the rounding
+// of the real quotient. Otherwise the one border between the two candidates is
+// compared exactly: the sign of a fused multiply-add is that of the unrounded sum.
+constexpr float kBelow = 1.0f - 0x1p-20f;
+constexpr float kAbove = 1.0f + 0x1p-20f;
+
+// amax / (6 g) in E4M3; inv6g is 1 / (6 g) to fp32.
+__device__ __forceinline__ uint32_t nv_scale(float amax, float g, float inv6g) {
+  const float q = amax * inv6g;
+  const uint32_t both = cvt_e4m3x2(q * kBelow, q * kAbove);
+  const uint32_t lo = both & 0xFFu, hi = both >> 8;
+  if (lo == hi) return lo;
+  const float mid = 0.5f * (e4m3_value(lo) + e4m3_value(hi));  // 5 significant bits; times 6 still exact
+  const float d = fmaf(-6.0f * mid, g, amax);
+  if (d != 0.0f) return d > 0.0f ? hi : lo;
+  return (lo & 1u) ? hi : lo;
+}
+
+// Codes of eight values whose rounding is in doubt somewhere: `lo` and `hi` are the
+// candidates of every value.
+__device__ __noinline__ uint32_t nv_settle(const float (&v)[8], uint32_t lo, uint32_t hi, float s, float g) {
+  uint32_t out = lo;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = (lo >> (4 * i)) & 7u, b = (hi >> (4 * i)) & 7u;
+    if (a != b) {
+      const float border = 0.5f * (e2m1_value(a) + e2m1_value(b));
+      const float d = fmaf(-border * s, g, fabsf(v[i]));  // border * s is exact: 3 + 4 bits
+      const bool up = d > 0.0f || (d == 0.0f && (a & 1u));
+      if (up) out = (out & ~(15u << (4 * i))) | (hi & (15u << (4 * i)));
+    }
+  }
+  return out;
+}
+
+// NV: NVFP4, else MXFP4. One 32-byte piece of the input per thread and turn.
+template <typename T, bool NV>
+__global__ void __launch_bounds__(kThreads)
+    quantize_kernel(const T* __restrict__ x, const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
+                    uint8_t* __restrict__ scales, int64_t groups, int64_t pieces_per_group) {
+  constexpr int EPT = elems_per_thread<T>();
+  constexpr int TPB = (NV ? 16 : 32) / EPT;  // threads that share a block
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
+    float g = 1.0f, inv6g = 0.0f;
+    bool g_ok = true;
+    if constexpr (NV) {
+      if (tensor_scale != nullptr) g = tensor_scale[grp];
+      g_ok = g >= kMinTensorScale && g <= kMaxTensorScale;  // false for a NaN
+      inv6g = 1.0f / (6.0f * g);
+    }
+    const int64_t first = grp * pieces_per_group;
+    // whole warps stay in the loop together (the shuffles below are warp-wide)
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads; base < pieces_per_group;
+         base += static_cast<int64_t>(gridDim.x) * kThreads) {
+      const int64_t p = base + threadIdx.x;
+      const bool live = p < pieces_per_group;
+      float v[EPT];
+      if (live) {
+        load_row32(x + (first + p) * EPT, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+      }
+      // magnitudes compare as integers; an infinity or a NaN is above every number
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int o = 1; o < TPB; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool bad = top >= 0x7F800000u || !g_ok;
+      uint32_t sbyte;
+      float s, inv;
+      if constexpr (NV) {
+        sbyte = bad ? 0x7Fu : nv_scale(__uint_as_float(top), g, inv6g);
+        s = e4m3_value(sbyte);
+        inv = sbyte == 0 ? 0.0f : 1.0f / (s * g);
+      } else {
+        const uint32_t e = top >> 23;
+        sbyte = bad ? 0xFFu : (e < 2u ? 0u : e - 2u);
+        s = 0.0f;
+        inv = __uint_as_float((254u - (bad ? 127u : sbyte)) << 23);  // 2^(127 - sbyte): the products below are exact
+      }
+      uint32_t word[EPT / 8];
+#pragma unroll
+      for (int h = 0; h < EPT / 8; ++h) {
+        float q[8], t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = v[8 * h + i] * inv;
+        if constexpr (NV) {
+          float u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            t[i] = q[i] * kBelow;
+            u[i] = q[i] * kAbove;
+          }
+          const uint32_t lo = cvt_e2m1x8(t), hi = cvt_e2m1x8(u);
+          word[h] = lo;
+          if (lo != hi) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i];
+            word[h] = nv_settle(w, lo, hi, s, g);
+          }
+        } else {
+          word[h] = cvt_e2m1x8(q);
+        }
+        if (bad) word[h] = 0u;
+      }
+      if (live) {
+        if constexpr (EPT == 16)
+          *reinterpret_cast<uint2*>(codes + (first + p) * 8) = make_uint2(word[0], word[EPT / 8 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(codes + (first + p) * 4) = word[0];
+        if (TPB == 1 || (threadIdx.x & (TPB - 1)) == 0)
+          scales[(first + p) / TPB] = static_cast<uint8_t>(sbyte);
+      }
+    }
+  }
+}
+
+// Eight E2M1 codes (first in the lowest nibble) to fp32, times 2^-126: each field
+// is moved to the top of an fp32's exponent and mantissa, the sign to bit 31.
+__device__ __forceinline__ void e2m1x8_scaled(uint32_t w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t n = w >> (4 * i);
+    v[i] = __uint_as_float(((n & 7u) << 22) | ((n & 8u) << 28));
+  }
+}
+
+template <typename T, bool NV>
+__global__ void __launch_bounds__(kThreads)
+    dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                      const float* __restrict__ tensor_scale, T* __restrict__ out, int64_t groups,
+                      int64_t pieces_per_group) {
+  constexpr int EPT = elems_per_thread<T>();
+  constexpr int TPB = (NV ? 16 : 32) / EPT;
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
+    float g = 1.0f;
+    if (NV && tensor_scale != nullptr) g = tensor_scale[grp];
+    const int64_t first = grp * pieces_per_group;
+    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces_per_group;
+         p += static_cast<int64_t>(gridDim.x) * kThreads) {
+      const int64_t at = first + p;
+      uint32_t w[EPT / 8];
+      if constexpr (EPT == 16) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + at * 8));
+        w[0] = c.x;
+        w[EPT / 8 - 1] = c.y;
+      } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(codes + at * 4));
+      }
+      const uint32_t b = __ldg(scales + at / TPB) & (NV ? 0x7Fu : 0xFFu);
+      float s;
+      if constexpr (NV)
+        s = b == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(b);
+      else
+        s = b == 255u ? __uint_as_float(0x7FC00000u) : (b == 0u ? 0x1p-127f : __uint_as_float(b << 23));
+      float v[EPT];
+#pragma unroll
+      for (int h = 0; h < EPT / 8; ++h) {
+        float t[8];
+        e2m1x8_scaled(w[h], t);
+        // the first two products are exact (6 significant bits), so a value is rounded once
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = t[i] * 0x1p126f * s;
+          v[8 * h + i] = NV ? e * g : e;
+        }
+      }
+      uint4 o[2];
+      uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4)
+          ow[i] = __float_as_uint(v[i]);
+        else
+          ow[i] = pack_bf16x2(v[(2 * i) % EPT], v[(2 * i + 1) % EPT]);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(out + at * EPT);
+      dst[0] = o[0];
+      dst[1] = o[1];
+    }
+  }
+}
+
+// scale[group] = max(amax / 2688, 2^-100) over the finite elements: 2688 = 6 * 448
+// puts the largest block scale at E4M3's largest number. Division and the lower
+// bound keep the order of their arguments, so each CTA divides its own amax and the
+// largest result is the group's; non-negative fp32 numbers order as integers. With
+// one CTA a group it is stored, else combined by an integer atomic maximum (whose
+// order does not matter) over a zeroed array.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    tensor_scale_kernel(const T* __restrict__ x, float* __restrict__ scale, int64_t groups, int64_t pieces_per_group) {
+  constexpr int EPT = elems_per_thread<T>();
+  __shared__ uint32_t warp_top[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
+    const T* src = x + grp * pieces_per_group * EPT;
+    uint32_t top = 0;
+    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces_per_group;
+         p += static_cast<int64_t>(gridDim.x) * kThreads) {
+      float v[EPT];
+      load_row32(src + p * EPT, v);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+        top = max(top, m < 0x7F800000u ? m : 0u);
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 1; i < kThreads / 32; ++i) top = max(top, warp_top[i]);
+      const float s = fmaxf(__uint_as_float(top) / 2688.0f, kMinTensorScale);
+      if (gridDim.x == 1)
+        scale[grp] = s;
+      else
+        atomicMax(reinterpret_cast<unsigned int*>(scale + grp), __float_as_uint(s));
+    }
+    __syncthreads();
+  }
+}
+
+// CTAs: enough to fill the device (8 of 256 threads an SM), no more than there is
+// work for; a group each in y.
+dim3 piece_grid(int64_t groups, int64_t pieces_per_group, int per_sm) {
+  const int64_t want = static_cast<int64_t>(device_sm_count()) * per_sm;
+  const int64_t gy = groups < 65535 ? groups : 65535;
+  int64_t gx = (pieces_per_group + kThreads - 1) / kThreads;
+  const int64_t share = (want + gy - 1) / gy;
+  if (gx > share) gx = share;
+  return dim3(static_cast<unsigned>(gx < 1 ? 1 : gx), static_cast<unsigned>(gy));
+}
+
+}  // namespace
+
+cudaError_t launch_tensor_scale(int64_t groups, int64_t per_group, bool fp32, const void* x, float* scale,
+                                cudaStream_t st) {
+  const int64_t pieces = per_group / (fp32 ? 8 : 16);
+  const dim3 grid = piece_grid(groups, pieces, 8);
+  if (grid.x > 1) {
+    const cudaError_t e = cudaMemsetAsync(scale, 0, static_cast<size_t>(groups) * 4, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (fp32)
+    return launch_dependent(tensor_scale_kernel<float>, grid, dim3(kThreads), 0, st, nullptr, 0,
+                            static_cast<const float*>(x), scale, groups, pieces);
+  return launch_dependent(tensor_scale_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, nullptr, 0,
+                          static_cast<const __nv_bfloat16*>(x), scale, groups, pieces);
+}
+
+cudaError_t launch_quantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const void* x,
+                            const float* tensor_scale, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  const int64_t pieces = per_group / (fp32 ? 8 : 16);
+  const dim3 grid = piece_grid(groups, pieces, 8);
+  auto go = [&](auto kern, auto* typed) {
+    return launch_dependent(kern, grid, dim3(kThreads), 0, st, nullptr, 0, typed, tensor_scale, codes, scales, groups,
+                            pieces);
+  };
+  const float* xf = static_cast<const float*>(x);
+  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+  if (nv) return fp32 ? go(quantize_kernel<float, true>, xf) : go(quantize_kernel<__nv_bfloat16, true>, xb);
+  return fp32 ? go(quantize_kernel<float, false>, xf) : go(quantize_kernel<__nv_bfloat16, false>, xb);
+}
+
+cudaError_t launch_dequantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const uint8_t* codes,
+                              const uint8_t* scales, const float* tensor_scale, void* out, cudaStream_t st) {
+  const int64_t pieces = per_group / (fp32 ? 8 : 16);
+  const dim3 grid = piece_grid(groups, pieces, 8);
+  auto go = [&](auto kern, auto* typed) {
+    return launch_dependent(kern, grid, dim3(kThreads), 0, st, nullptr, 0, codes, scales, tensor_scale, typed, groups,
+                            pieces);
+  };
+  float* of = static_cast<float*>(out);
+  __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(out);
+  if (nv) return fp32 ? go(dequantize_kernel<float, true>, of) : go(dequantize_kernel<__nv_bfloat16, true>, ob);
+  return fp32 ? go(dequantize_kernel<float, false>, of) : go(dequantize_kernel<__nv_bfloat16, false>, ob);
+}
+
+}  // namespace moe

@@ -235,7 +235,143 @@ moe_status ec_prepare(const moe_config* cfg, int64_t capacity, void* ws, size_t 
 
 }  // namespace
 
+namespace {
+
+// Checks shared by the ragged products (the device is looked at last, by the caller); `k_unit` is the multiple that k must be of.
+moe_status grouped_prepare(const moe_grouped_shape* s, int k_unit, const int32_t* offsets, void* ws, size_t ws_bytes) {
+  if (s == nullptr || offsets == nullptr) return MOE_ERR_INVALID_ARG;
+  if (s->out_dtype != MOE_BF16 && s->out_dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  if (s->rows < 0 || s->rows > (int64_t(1) << 28) || s->n_experts < 1 || s->n_experts > kMaxExperts || s->n < 8 ||
+      s->n > 32768 || s->n % 8 != 0 || s->k < 8 || s->k > 32768 || s->k % k_unit != 0)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_grouped_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return MOE_OK;
+}
+
+// A 16-byte aligned buffer; one of no rows may be NULL.
+bool usable(const void* p, int64_t rows) { return (p != nullptr || rows == 0) && aligned16(p); }
+
+// Checks shared by the 4-bit conversions; *count receives the elements of a group.
+moe_status microscaled_prepare(int32_t format, int64_t groups, int64_t rows, int64_t cols, int32_t dtype,
+                               const float* tensor_scale, int64_t* count) {
+  if (format != MOE_MXFP4 && format != MOE_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16 && dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  if (format == MOE_MXFP4 && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
+  const int64_t most = int64_t(1) << 40;
+  if (groups < 1 || groups > most || rows < 0 || rows > most || cols < 32 || cols > (1 << 20) || cols % 32 != 0 ||
+      (rows > 0 && (groups > most / cols || groups * cols > most / rows)))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  *count = rows * cols;
+  return MOE_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+size_t moe_grouped_workspace_bytes(void) { return 256; }
+
+moe_status moe_grouped_gemm(const moe_grouped_shape* shape, const void* x, const int32_t* group_start,
+                            const int32_t* offsets, const void* w, void* y, void* ws, size_t ws_bytes,
+                            cudaStream_t stream) {
+  const moe_status r = grouped_prepare(shape, 8, offsets, ws, ws_bytes);
+  if (r != MOE_OK) return r;
+  if (!usable(x, shape->rows) || !usable(w, 1) || !usable(y, shape->rows)) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  if (shape->rows == 0) return MOE_OK;
+  MOE_TRY(launch_ragged_forward(shape->rows, shape->n_experts, shape->n, shape->k, shape->out_dtype == MOE_FP32, x,
+                                group_start, offsets, w, y, at<int32_t>(ws, 0), stream));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const void* dy, const int32_t* group_start,
+                                  const int32_t* offsets, const void* w, void* dx, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  const moe_status r = grouped_prepare(shape, 8, offsets, ws, ws_bytes);
+  if (r != MOE_OK) return r;
+  if (!usable(dy, shape->rows) || !usable(w, 1) || !usable(dx, shape->rows)) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  if (shape->rows == 0) return MOE_OK;
+  MOE_TRY(launch_ragged_dgrad(shape->rows, shape->n_experts, shape->n, shape->k, shape->out_dtype == MOE_FP32, dy,
+                              group_start, offsets, w, dx, at<int32_t>(ws, 0), stream));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, const void* x,
+                                  const int32_t* group_start, const int32_t* offsets, void* dw, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  const moe_status r = grouped_prepare(shape, 8, offsets, ws, ws_bytes);
+  if (r != MOE_OK) return r;
+  if (!usable(dy, shape->rows) || !usable(x, shape->rows) || !usable(dw, 1)) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  if (shape->rows == 0) {
+    const size_t count = static_cast<size_t>(shape->n_experts) * shape->n * shape->k;
+    MOE_TRY(cudaMemsetAsync(dw, 0, count * (shape->out_dtype == MOE_FP32 ? 4 : 2), stream));
+    return MOE_OK;
+  }
+  MOE_TRY(launch_ragged_wgrad(shape->rows, shape->n_experts, shape->n, shape->k, shape->out_dtype == MOE_FP32, dy, x,
+                              group_start, offsets, dw, at<int32_t>(ws, 0), stream));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_microscaled(const moe_grouped_shape* shape, int32_t format, const uint8_t* x_codes,
+                                        const uint8_t* x_scales, const float* x_scale, const int32_t* group_start,
+                                        const int32_t* offsets, const uint8_t* w_codes, const uint8_t* w_scales,
+                                        const float* w_scale, void* y, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream) {
+  if (format != MOE_MXFP4 && format != MOE_NVFP4) return MOE_ERR_INVALID_ARG;
+  const moe_status r = grouped_prepare(shape, 32, offsets, ws, ws_bytes);
+  if (r != MOE_OK) return r;
+  if (!usable(x_codes, shape->rows) || !usable(x_scales, shape->rows) || !usable(w_codes, 1) || !usable(w_scales, 1) ||
+      !usable(y, shape->rows) || (format == MOE_MXFP4 && (x_scale != nullptr || w_scale != nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  if (shape->rows == 0) return MOE_OK;
+  MOE_TRY(launch_ragged_microscaled(format == MOE_NVFP4, shape->rows, shape->n_experts, shape->n, shape->k,
+                                    shape->out_dtype == MOE_FP32, x_codes, x_scales, x_scale, group_start, offsets,
+                                    w_codes, w_scales, w_scale, y, at<int32_t>(ws, 0), stream));
+  return MOE_OK;
+}
+
+moe_status moe_tensor_scale_microscaled(int64_t groups, int64_t rows, int64_t cols, int32_t dtype, const void* x,
+                                        float* scale, cudaStream_t stream) {
+  int64_t count = 0;
+  const moe_status r = microscaled_prepare(MOE_NVFP4, groups, rows, cols, dtype, nullptr, &count);
+  if (r != MOE_OK) return r;
+  if (!usable(x, rows) || scale == nullptr) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  MOE_TRY(launch_tensor_scale(groups, count, dtype == MOE_FP32, x, scale, stream));
+  return MOE_OK;
+}
+
+moe_status moe_quantize_microscaled(int32_t format, int64_t groups, int64_t rows, int64_t cols, int32_t dtype,
+                                    const void* x, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                                    cudaStream_t stream) {
+  int64_t count = 0;
+  const moe_status r = microscaled_prepare(format, groups, rows, cols, dtype, tensor_scale, &count);
+  if (r != MOE_OK) return r;
+  if (!usable(x, rows) || !usable(codes, rows) || !usable(scales, rows)) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(launch_quantize(format == MOE_NVFP4, groups, count, dtype == MOE_FP32, x, tensor_scale, codes, scales,
+                          stream));
+  return MOE_OK;
+}
+
+moe_status moe_dequantize_microscaled(int32_t format, int64_t groups, int64_t rows, int64_t cols, int32_t dtype,
+                                      const uint8_t* codes, const uint8_t* scales, const float* tensor_scale,
+                                      void* out, cudaStream_t stream) {
+  int64_t count = 0;
+  const moe_status r = microscaled_prepare(format, groups, rows, cols, dtype, tensor_scale, &count);
+  if (r != MOE_OK) return r;
+  if (!usable(out, rows) || !usable(codes, rows) || !usable(scales, rows)) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(launch_dequantize(format == MOE_NVFP4, groups, count, dtype == MOE_FP32, codes, scales, tensor_scale, out,
+                            stream));
+  return MOE_OK;
+}
 
 const char* moe_status_string(int32_t status) {
   switch (status) {

@@ -187,5 +187,36 @@ cudaError_t raise_smem_limit(const void* func, size_t bytes, std::atomic<size_t>
 // [box_rows, box_cols] box and 128-byte swizzle (out-of-range boxes read zeros).
 bool make_map(CUtensorMap* m, const void* base, bool fp32, uint64_t rows, uint64_t cols, uint32_t box_cols,
               uint32_t box_rows);
+// 3-D descriptors, 128-byte swizzle: bf16 matrices [mats, rows, cols], and packed
+// 4-bit codes [mats, rows, row_bytes] in boxes 128 bytes wide. A box that leaves a
+// matrix in any dimension reads zeros there.
+bool make_map_3d(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                 uint32_t box_rows);
+bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows, uint64_t row_bytes,
+                    uint32_t box_rows);
+
+// Ragged products grouped by expert (ragged_gemm.cu): y = W_e x, dx = W_e^T dy,
+// dW_e = sum dy x^T over rows [start_e, start_e + count_e) of buffers of `rows` rows.
+cudaError_t launch_ragged_forward(int64_t rows, int E, int n, int k, bool out32, const void* x, const int32_t* gs,
+                                  const int32_t* off, const void* w, void* y, int32_t* status, cudaStream_t st);
+cudaError_t launch_ragged_dgrad(int64_t rows, int E, int n, int k, bool out32, const void* dy, const int32_t* gs,
+                                const int32_t* off, const void* w, void* dx, int32_t* status, cudaStream_t st);
+cudaError_t launch_ragged_wgrad(int64_t rows, int E, int n, int k, bool out32, const void* dy, const void* x,
+                                const int32_t* gs, const int32_t* off, void* dw, int32_t* status, cudaStream_t st);
+// Columns of an output tile (256, 128 or 64) for `row_tiles` 128-row tiles.
+int pick_tile_width(int64_t row_tiles, int cols);
+// The same product on 4-bit operands (microscaled_gemm.cu).
+cudaError_t launch_ragged_microscaled(bool nv, int64_t rows, int E, int n, int k, bool out32, const uint8_t* xc,
+                                      const uint8_t* xs, const float* xg, const int32_t* gs, const int32_t* off,
+                                      const uint8_t* wc, const uint8_t* ws, const float* wg, void* y, int32_t* status,
+                                      cudaStream_t st);
+
+// Microscaled 4-bit values (microscaled.cu). per_group: elements of a group.
+cudaError_t launch_tensor_scale(int64_t groups, int64_t per_group, bool fp32, const void* x, float* scale,
+                                cudaStream_t st);
+cudaError_t launch_quantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const void* x,
+                            const float* tensor_scale, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+cudaError_t launch_dequantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const uint8_t* codes,
+                              const uint8_t* scales, const float* tensor_scale, void* out, cudaStream_t st);
 
 }  // namespace moe

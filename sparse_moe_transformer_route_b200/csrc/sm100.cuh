@@ -22,6 +22,7 @@ enum DeviceCode : int32_t {
   DEV_WAIT_TIMEOUT_GRID = 0x105,
   DEV_BAD_EXPERT_INDEX = 0x201,
   DEV_COUNT_MISMATCH = 0x202,
+  DEV_BAD_GROUP = 0x203,
 };
 
 // Upper bound on any single wait inside a kernel: about one second.
