@@ -59,6 +59,7 @@ struct QCfg {
   static constexpr size_t SMEM_BYTES = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + MISC_BYTES;
   static constexpr int AHEAD = 4;  // stages whose scales are in flight in registers
   static_assert(STAGES >= 3, "ring");
+  static_assert(SMEM_BYTES > 114 * 1024, "one CTA an SM");
   static_assert(SFB_COL + WORDS * 4 * BBLK <= 512, "TMEM columns");
   static_assert(BN == 256 || BN == 128 || BN == 64, "tile N");
 };

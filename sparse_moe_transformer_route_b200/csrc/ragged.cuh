@@ -65,6 +65,73 @@ __device__ __forceinline__ int tile_expert(const RaggedGroups& g, int E, int mt)
   return lo;
 }
 
+// Issuing MMAs. One thread feeds the tensor core, and its own instructions bound the rate
+// when each MMA's operands are put together by divergent code: 230 cycles an MMA of 256 x
+// 256 x 16 that the tensor cores take 128 for (measured with the loads taken out). So
+//  - the high word of a descriptor is a constant, the low word (address and leading
+//    offset) is carried from stage to stage, and a step adds a constant to it (195);
+//  - the whole warp runs the loop on values that the compiler can see to be the same in
+//    every lane (uniform()), and one lane is elected around the instructions alone, so
+//    that their operands live in uniform registers (150).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+struct DescLo {
+  uint32_t a, b;
+};
+
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void umma_bf16_lo(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                             uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
+        : "memory");
+}
+
+// The MMAs of a stage of four steps, `steps` of them (fewer at a reduction's end).
+// A_STEP, B_STEP: bytes between the steps' operands.
+template <bool PAIR, int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_stage(uint32_t d, DescLo lo, uint32_t idesc, bool first, int steps) {
+  umma_bf16_lo<PAIR>(d, lo.a, lo.b, idesc, first ? 0u : 1u);
+  if (steps == 4) {
+#pragma unroll
+    for (int kk = 1; kk < 4; ++kk)
+      umma_bf16_lo<PAIR>(d, lo.a + kk * (A_STEP >> 4), lo.b + kk * (B_STEP >> 4), idesc, 1u);
+  } else {
+    for (int kk = 1; kk < steps; ++kk)
+      umma_bf16_lo<PAIR>(d, lo.a + kk * (A_STEP >> 4), lo.b + kk * (B_STEP >> 4), idesc, 1u);
+  }
+}
+
 // 3-D tiled load global -> shared, completion counted on `bar`; c0 is the innermost coordinate.
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t c0, int32_t c1,
                                             int32_t c2) {
@@ -73,6 +140,45 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
+}
+
+// The same by a CTA of a pair, its bytes counted on the leader's barrier (see tma_load_2d_pair).
+__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t c0,
+                                                 int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Arrival on another CTA's barrier that orders this thread's earlier writes for whoever
+// waits there with cluster scope.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// mbar_wait whose completion orders what the arrivals of both CTAs released.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t spins = 0;
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (((++spins) & 255u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
 }
 
 // One warp writes a 32 x 32 chunk whose row `lane` this thread holds in v, through
