@@ -3,22 +3,34 @@
 // with the block-scaled form of tcgen05.mma: 64 terms an instruction, codes packed
 // two to a byte in shared memory, block scales in TMEM, fp32 accumulation. The
 // products of scaled elements are exact there; the two tensor scales multiply the
-// finished sum.
+// finished sum. As in ragged_gemm.cu the weight is the MMA's M operand and the rows its
+// N operand, of any multiple of 16 rows.
 //
 // Scales. The instruction reads the scale bytes of row r (of either operand) from
 // TMEM lane r % 32, column r / 32, four bytes a column: with NVFP4 the four blocks of
 // one 64-term step, with MXFP4 the four blocks of two steps. One tcgen05.cp
 // (32x128b.warpx4) brings 128 rows' column set from 512 bytes of shared memory whose
 // 16-byte line i holds the words of rows i, i + 32, i + 64, i + 96. In global memory
-// scales are plain row-major bytes, so that a group may start at any row: loader
-// warps read 16 (NVFP4) or 8 (MXFP4) bytes of four rows per thread, which is one
-// stage of 256 terms, and write the lines as they are: 16-byte loads and stores, no
-// bank conflicts. The loads run several stages ahead in registers.
+// scales are plain row-major bytes, so that a group may start at any row. TMA brings
+// 32 bytes of each row, the scales of two stages of 256 terms (NVFP4) or four (MXFP4),
+// and a warp per 128 rows turns its 4 KB round in place: 16-byte reads and stores, no
+// bank conflicts (32-byte swizzle). Loading them through registers instead is slow
+// (32768 rows
+// of 2048 x 2048: 227 us, 68 this way): the fence in front of the tensor core's reads waits for every load that the
+// warp has in flight. Only widths whose scale rows are no multiple of 16 bytes, which
+// TMA cannot address, go that way.
 //
 // Structure per CTA (persistent, one an SM): warp 0 TMA of codes, warp 1 MMA issue,
 // warps 2..9 epilogue, the rest scale loaders. A 256-column accumulator pair and the
 // scales do not fit TMEM's 512 columns side by side, so the two accumulators share
 // 64 columns: the epilogue reads those first and then lets the next tile start.
+// PAIR: a tile of 256 output columns on the two CTAs of a cluster, each with its 128 rows
+// of the weight and half of the tile's rows in shared memory and the scales of its own
+// 128 weight rows and of all the tile's rows; the leader issues cta_group::2 copies and
+// MMAs for both.
+// The scale warps arrive on the leader's barrier without a cluster-scope release: each
+// CTA's lines are read from its own shared memory by its own tensor core (with one,
+// 32768 rows of 2048 x 2048 took 141 us instead of 86).
 // Every wait is bounded; a timeout is recorded in the status word.
 #include <cudaTypedefs.h>
 
@@ -27,23 +39,28 @@
 namespace moe {
 namespace {
 
-template <bool NV_, int BN_, bool O32_>
+template <bool NV_, int BN_, bool O32_, bool PAIR_>
 struct QCfg {
   static constexpr bool NV = NV_;
   static constexpr int BN = BN_;
   static constexpr bool O32 = O32_;
+  static constexpr bool PAIR = PAIR_;
   using OutT = std::conditional_t<O32, float, __nv_bfloat16>;
-  static constexpr int BM = 128;
+  static constexpr int CTAS = PAIR ? 2 : 1;
+  static constexpr int BM = 128 * CTAS;          // M: output columns a tile; BN: at most so many rows
+  static constexpr int UNIT = 16 * CTAS;         // N is a multiple of this
   static constexpr int BK = 256;                 // terms a stage: one 128-byte swizzle row of codes
   static constexpr int UK = 64;                  // terms a tcgen05.mma
   static constexpr int SCALE_BYTES = NV ? 16 : 8;  // scale bytes of a row and stage
   static constexpr int WORDS = SCALE_BYTES / 4;  // TMEM column sets a stage
+  static constexpr int SF_STAGES_PER = NV ? 2 : 4;  // stages whose scales fill a slot
+  static constexpr int SF_BLOCK = 4096;          // 128 rows' scales of a slot: 8 words a row
   static constexpr int BBLK = (BN + 127) / 128;  // 128-row blocks of B
-  static constexpr int A_BYTES = BM * 128;
-  static constexpr int B_BYTES = BN * 128;
-  static constexpr int SFA_BYTES = WORDS * 512;
-  static constexpr int SFB_BYTES = WORDS * 512 * BBLK;
-  static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES + 1023) / 1024 * 1024;
+  static constexpr int B_ROWS = BN / CTAS;       // rows of B in this CTA's shared memory
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = B_ROWS * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int SF_BYTES = (1 + BBLK) * SF_BLOCK;  // a slot
   static constexpr bool OVERLAP = BN == 256;
   static constexpr uint32_t ACC1 = OVERLAP ? 192 : BN;  // first column of the second accumulator
   static constexpr uint32_t SFA_COL = 448;
@@ -51,17 +68,22 @@ struct QCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int EPI_WARPS = 8;
   static constexpr int SF_WARPS = 1 + BBLK;
-  static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS);
-  static constexpr int CHUNKS = BN / 64;  // 32-column chunks of an epilogue warp
+  static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS + 1);
+  static constexpr int CHUNKS = (BN + 63) / 64;  // 32-column chunks of an epilogue warp
   static constexpr int MISC_BYTES = 1024 + static_cast<int>(sizeof(RaggedGroups));
-  static constexpr int STAGES_FIT = (227 * 1024 - 1024 - MISC_BYTES) / STAGE_BYTES;
+  static constexpr int ROOM = 227 * 1024 - 1024 - MISC_BYTES;
+  static constexpr int STAGES_FIT = (ROOM - (PAIR ? 5 : 2) * SF_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
-  static constexpr size_t SMEM_BYTES = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + MISC_BYTES;
-  static constexpr int AHEAD = 4;  // stages whose scales are in flight in registers
-  static_assert(STAGES >= 3, "ring");
+  // the scales' way is longer by a pass through registers: their ring reaches further
+  static constexpr int SF_FIT = (ROOM - STAGES * STAGE_BYTES) / SF_BYTES;
+  static constexpr int SF_SLOTS = SF_FIT > 8 ? 8 : SF_FIT;
+  static constexpr size_t SMEM_BYTES =
+      1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + static_cast<size_t>(SF_SLOTS) * SF_BYTES + MISC_BYTES;
+  static constexpr int AHEAD = 2;  // slots whose scales one batch of loads brings to registers
+  static_assert(STAGES >= 3 && SF_SLOTS >= 2 && (2 * STAGES + 3 * SF_SLOTS + 6) * 8 <= 1024, "rings");
   static_assert(SMEM_BYTES > 114 * 1024, "one CTA an SM");
   static_assert(SFB_COL + WORDS * 4 * BBLK <= 512, "TMEM columns");
-  static_assert(BN == 256 || BN == 128 || BN == 64, "tile N");
+  static_assert(BN == 256 || (!PAIR && (BN == 128 || BN == 64 || BN == 32)), "tile N");
 };
 
 struct QArgs {
@@ -73,6 +95,7 @@ struct QArgs {
   const float* w_scale;
   int64_t rows;
   int E, n, k;
+  bool tma_scales;  // scale rows are multiples of 16 bytes
   void* out;
   int32_t* status;
 };
@@ -86,194 +109,235 @@ __host__ __device__ constexpr uint32_t micro_idesc(bool nv, int M, int N, uint32
          ((static_cast<uint32_t>(M) >> 7) << 27) | (sf_id << 29);
 }
 
-// Descriptor of a scale block in shared memory: no swizzle, 8-row groups of 16-byte
-// lines 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
-}
-
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-template <bool NV>
-__device__ __forceinline__ void umma_micro(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t accumulate) {
-  if constexpr (NV)
+// 128 rows' words from shared memory to TMEM. Descriptor of a scale block: no swizzle,
+// 8-row groups of 16-byte lines 128 bytes apart; `lo` is its address >> 4.
+template <bool PAIR>
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t lo) {
+  constexpr uint32_t hi = (128u >> 4) | (1u << 14);
+  if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-            d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}\n" ::"r"(taddr),
+        "r"(lo), "r"(hi)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-            d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}\n" ::"r"(taddr),
+        "r"(lo), "r"(hi)
         : "memory");
 }
 
+#define MOE_UMMA_MICRO(GROUP, VEC)                                                                            \
+  asm volatile(                                                                                               \
+      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"                                                           \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                             \
+      "mov.b64 ad, {%1, %7};\n\tmov.b64 bd, {%2, %7};\n\t"                                                    \
+      "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                           \
+      " [%0], ad, bd, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),                                                    \
+      "r"(alo), "r"(blo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescHiSw128)                  \
+      : "memory")
+
+template <bool NV, bool PAIR>
+__device__ __forceinline__ void umma_micro(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate) {
+  if constexpr (PAIR) {
+    if constexpr (NV) MOE_UMMA_MICRO("2", "4X");
+    else MOE_UMMA_MICRO("2", "2X");
+  } else {
+    if constexpr (NV) MOE_UMMA_MICRO("1", "4X");
+    else MOE_UMMA_MICRO("1", "2X");
+  }
+}
+#undef MOE_UMMA_MICRO
+
 struct QTile {
-  int e, m0, n0, valid;
+  int e;
+  int m0;    // first output column
+  int n0;    // first row of the buffer
+  int left;  // rows, of the group
+  int N;     // the MMA's N
 };
 
 template <class C>
-__device__ __forceinline__ QTile q_tile(const QArgs& a, const RaggedGroups& g, int nN, int L) {
+__device__ __forceinline__ QTile q_tile(const QArgs& a, const RaggedGroups& g, int nM, int L) {
   QTile t;
-  const int mt = L / nN;
-  t.n0 = (L - mt * nN) * C::BN;
-  t.e = tile_expert(g, a.E, mt);
-  const int in = (mt - g.tiles[t.e]) * C::BM;
-  t.m0 = g.start[t.e] + in;
-  t.valid = min(C::BM, g.count[t.e] - in);
+  const int place = tile_place(g, a.E, L);
+  t.e = g.order[place];
+  const int in = L - g.tiles[place];
+  const int rt = in / nM;
+  t.m0 = (in - rt * nM) * C::BM;
+  const int count = g.count[t.e];
+  const int per = rows_a_tile<C::BN, C::UNIT>(count);
+  t.n0 = g.start[t.e] + rt * per;
+  t.left = min(per, count - rt * per);
+  t.N = (t.left + C::UNIT - 1) / C::UNIT * C::UNIT;
   return t;
 }
 
-// The scale words of one row for one stage: bytes [at, at + 4 WORDS) of its scale
-// row, zero past the row's end. `whole`: every stage of a row is a full, aligned piece.
-template <int WORDS>
-__device__ __forceinline__ void load_scale_words(uint32_t (&w)[WORDS], const uint8_t* row, int at, int row_bytes,
-                                                 bool whole) {
-  if (whole) {
-    if constexpr (WORDS == 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + at));
-      w[0] = v.x;
-      w[1] = v.y;
-      w[2] = v.z;
-      w[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + at));
-      w[0] = v.x;
-      w[1] = v.y;
-    }
-  } else {
+// N words of a scale row from byte `at` on, zero past the row's end. The row starts at
+// any address: the words that cover the piece are read at multiples of four and shifted
+// together, but for what would lie past `end`, the buffer's end, which is read byte by
+// byte.
+template <int N>
+__device__ __forceinline__ void load_scale_words(uint32_t (&w)[N], const uint8_t* row, int at, int row_bytes,
+                                                 const uint8_t* end) {
+  const uint8_t* p = row + at;
+  const int bytes = min(4 * N, row_bytes - at);
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+  const uint8_t* base = p - off;
+  uint32_t v[N + 1];
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c = at + 4 * i + b;
-        if (c < row_bytes) v |= static_cast<uint32_t>(__ldg(row + c)) << (8 * b);
+  for (int i = 0; i <= N; ++i) {
+    v[i] = 0u;
+    if (4 * i < bytes + static_cast<int>(off)) {
+      if (base + 4 * i + 4 <= end) {
+        v[i] = __ldg(reinterpret_cast<const uint32_t*>(base) + i);
+      } else {
+        for (int b = 0; b < 4; ++b)
+          if (base + 4 * i + b < end) v[i] |= static_cast<uint32_t>(__ldg(base + 4 * i + b)) << (8 * b);
       }
-      w[i] = v;
     }
   }
-}
-
-// 32 consecutive columns of one row, this thread's, scaled and stored in pieces of 16
-// bytes; `cols` (a multiple of 8) bounds them.
-template <typename T>
-__device__ __forceinline__ void store_row32(T* dst, const uint32_t (&r)[32], float alpha, int cols) {
-  constexpr int EPS = 16 / static_cast<int>(sizeof(T));
 #pragma unroll
-  for (int i = 0; i < 32 / EPS; ++i) {
-    uint4 w;
-    if constexpr (sizeof(T) == 4) {
-      w.x = __float_as_uint(__uint_as_float(r[4 * i]) * alpha);
-      w.y = __float_as_uint(__uint_as_float(r[4 * i + 1]) * alpha);
-      w.z = __float_as_uint(__uint_as_float(r[4 * i + 2]) * alpha);
-      w.w = __float_as_uint(__uint_as_float(r[4 * i + 3]) * alpha);
-    } else {
-      w.x = pack_bf16x2(__uint_as_float(r[(8 * i) & 31]) * alpha, __uint_as_float(r[(8 * i + 1) & 31]) * alpha);
-      w.y = pack_bf16x2(__uint_as_float(r[(8 * i + 2) & 31]) * alpha, __uint_as_float(r[(8 * i + 3) & 31]) * alpha);
-      w.z = pack_bf16x2(__uint_as_float(r[(8 * i + 4) & 31]) * alpha, __uint_as_float(r[(8 * i + 5) & 31]) * alpha);
-      w.w = pack_bf16x2(__uint_as_float(r[(8 * i + 6) & 31]) * alpha, __uint_as_float(r[(8 * i + 7) & 31]) * alpha);
-    }
-    if (i * EPS < cols) reinterpret_cast<uint4*>(dst)[i] = w;
+  for (int i = 0; i < N; ++i) {
+    w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+    const int have = bytes - 4 * i;  // bytes of this word that belong to the row
+    if (have < 4) w[i] &= have <= 0 ? 0u : (1u << (8 * have)) - 1u;
   }
 }
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    microscaled_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
-                            const __grid_constant__ CUtensorMap tmB, const QArgs a) {
+    microscaled_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                            const __grid_constant__ CUtensorMap tmB32, const __grid_constant__ CUtensorMap tmSA,
+                            const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmSB32,
+                            const QArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(C::STAGES) * C::STAGE_BYTES);
+  unsigned char* sf_base = smem + static_cast<size_t>(C::STAGES) * C::STAGE_BYTES;
+  unsigned char* misc = sf_base + static_cast<size_t>(C::SF_SLOTS) * C::SF_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
   uint64_t* empty = full + C::STAGES;
-  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* sf_raw = empty + C::STAGES;  // a stage's scales have landed as they lie in global memory
+  uint64_t* sf_full = sf_raw + C::SF_SLOTS;
+  uint64_t* sf_empty = sf_full + C::SF_SLOTS;
+  uint64_t* acc_full = sf_empty + C::SF_SLOTS;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
-  RaggedGroups* groups =
-      reinterpret_cast<RaggedGroups*>(smem + static_cast<size_t>(C::STAGES) * C::STAGE_BYTES + 1024);
+  RaggedGroups* groups = reinterpret_cast<RaggedGroups*>(misc + 1024);
 
+  constexpr int CTAS = C::CTAS;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = C::PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool leader = rank == 0;
 
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1 + C::SF_WARPS);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::SF_SLOTS; ++s) {
+      mbar_init(&sf_raw[s], 1);
+      mbar_init(&sf_full[s], CTAS * C::SF_WARPS);
+      mbar_init(&sf_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], C::EPI_WARPS);
+      mbar_init(&acc_empty[b], CTAS * C::EPI_WARPS);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmA32);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmB32);
+    if (a.tma_scales) {
+      tma_prefetch_desc(&tmSA);
+      tma_prefetch_desc(&tmSB);
+      tma_prefetch_desc(&tmSB32);
+    }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, C::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (C::PAIR) {
+      tmem_alloc_pair(tmem_holder, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   __syncwarp();
   pdl_wait();
-  load_groups<C::BM>(groups, a.group_start, a.offsets, a.E, a.rows, a.status);
+  const int nM = (a.n + C::BM - 1) / C::BM;
+  load_groups<C::BN, C::UNIT, false>(groups, a.group_start, a.offsets, a.E, a.rows, nM, a.status);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (C::PAIR)
+    cluster_sync_all();
+  else
+    __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
-  const int nN = (a.n + C::BN - 1) / C::BN;
-  const int n_tiles = groups->tiles[a.E] * nN;
+  const uint32_t tmem_base = uniform(*tmem_holder);
+  const int n_tiles = uniform(groups->tiles[a.E]);
   const int nk = (a.k + C::BK - 1) / C::BK;
-  const int grid = static_cast<int>(gridDim.x);
+  const int first_tile = static_cast<int>(blockIdx.x) / CTAS;
+  const int grid = static_cast<int>(gridDim.x) / CTAS;
+  // barriers that the leader's MMA warp waits on
+  const uint32_t sf_full_leader = C::PAIR ? mapa_shared(smem_u32(sf_full), 0) : smem_u32(sf_full);
+  const uint32_t acc_empty_leader = C::PAIR ? mapa_shared(smem_u32(acc_empty), 0) : smem_u32(acc_empty);
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer of codes
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
-      bool ok = true;
-      for (int L = blockIdx.x; L < n_tiles && ok; L += grid) {
-        const QTile t = q_tile<C>(a, *groups, nN, L);
-        const int boxes = t.valid > 96 ? 0 : (t.valid + 31) / 32;
-        const uint32_t bytes = C::B_BYTES + (boxes == 0 ? C::A_BYTES : boxes * 32 * 128);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u)) {
-            report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    bool ok = true;
+    for (int L = first_tile; L < n_tiles && ok; L += grid) {
+      const QTile t = q_tile<C>(a, *groups, nM, L);
+      // few rows: 32-row boxes over those that count
+      const int need = uniform(t.N) / CTAS;
+      const int boxes = need > C::B_ROWS - 32 ? 0 : (need + 31) / 32;
+      const uint32_t bytes = C::A_BYTES + (boxes == 0 ? C::B_BYTES : boxes * 32 * 128);
+      const int row = uniform(t.n0) + need * rank;
+      const int col = uniform(t.m0) + 128 * rank;
+      const int e = uniform(t.e);
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u))) {
+          if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           unsigned char* sa = smem + static_cast<size_t>(stage) * C::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], bytes);
+          if (leader) mbar_arrive_expect_tx(&full[stage], CTAS * bytes);
+          auto load = [&](const CUtensorMap* map, unsigned char* dst, int c1, int c2) {
+            if constexpr (C::PAIR)
+              tma_load_3d_pair(map, &full[stage], dst, kb * 128, c1, c2);
+            else
+              tma_load_3d(map, &full[stage], dst, kb * 128, c1, c2);
+          };
+          load(&tmA, sa, col, e);
           if (boxes == 0) {
-            tma_load_3d(&tmA, &full[stage], sa, kb * 128, t.m0, 0);
+            load(&tmB, sa + C::A_BYTES, row, 0);
           } else {
-            for (int q = 0; q < boxes; ++q)
-              tma_load_3d(&tmA32, &full[stage], sa + q * (32 * 128), kb * 128, t.m0 + 32 * q, 0);
-          }
-          tma_load_3d(&tmB, &full[stage], sa + C::A_BYTES, kb * 128, t.n0, t.e);
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            for (int q = 0; q < boxes; ++q) load(&tmB32, sa + C::A_BYTES + q * (32 * 128), row + 32 * q, 0);
           }
         }
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // every copy this thread issued has landed before the CTA may end
+    }
+    // every copy has landed before the CTA may end (a pair's are counted by the
+    // leader; its peer waits at the cluster barrier)
+    if (leader) {
       for (int s = 0; s < C::STAGES && s < issued; ++s) {
         const int last = (issued - 1 - s) / C::STAGES;
         if (!mbar_wait(&full[s], static_cast<uint32_t>(last & 1))) report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
@@ -281,12 +345,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (leader) {
+      const uint32_t sf_lo = smem_u32(sf_base) >> 4;
+      const DescLo desc0{desc_lo_sw128(smem_u32(smem), 16), desc_lo_sw128(smem_u32(smem) + C::A_BYTES, 16)};
       int stage = 0;
       uint32_t phase = 0;
+      int slot = 0;
+      uint32_t sf_phase = 0;
       int tile = 0;
       bool ok = true;
-      for (int L = blockIdx.x; L < n_tiles && ok; L += grid, ++tile) {
+      for (int L = first_tile; L < n_tiles && ok; L += grid, ++tile) {
         const int acc = tile & 1;
         // the accumulator is free: with shared columns once the tile before has let
         // go of them (its epilogue is then past the tile before that)
@@ -296,52 +364,84 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         } else {
           free = mbar_wait(&acc_empty[acc], static_cast<uint32_t>(((tile >> 1) & 1) ^ 1));
         }
-        if (!free) {
-          report(a.status, DEV_WAIT_TIMEOUT_MMA);
+        if (!__all_sync(0xffffffffu, free)) {
+          if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_MMA);
           break;
         }
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
+        const uint32_t n_bits = uniform(static_cast<uint32_t>(q_tile<C>(a, *groups, nM, L).N) >> 3 << 17);
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&full[stage], phase)) {
-            report(a.status, DEV_WAIT_TIMEOUT_MMA);
+          const int sub = kb % C::SF_STAGES_PER;
+          if (!__all_sync(0xffffffffu,
+                          (sub != 0 || mbar_wait(&sf_full[slot], sf_phase)) && mbar_wait(&full[stage], phase))) {
+            if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_MMA);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + static_cast<size_t>(stage) * C::STAGE_BYTES);
-          const uint32_t sb = sa + C::A_BYTES;
-          const uint32_t sfa = sb + C::B_BYTES;
-          const uint32_t sfb = sfa + C::SFA_BYTES;
-          // copies and MMAs of one thread run in the order of their issue, so the
-          // columns can be written again for every stage
+          const bool slot_done = sub == C::SF_STAGES_PER - 1 || kb + 1 == nk;
+          if (elect_one()) {
+            const uint32_t off = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
+            const uint32_t sfa =
+                (sf_lo + static_cast<uint32_t>(slot) * (C::SF_BYTES >> 4) + sub * (C::WORDS * 512 >> 4)) & 0x3FFFu;
+            const uint32_t sfb = sfa + (C::SF_BLOCK >> 4);
+            // copies and MMAs of one thread run in the order of their issue, so the
+            // columns can be written again for every stage
 #pragma unroll
-          for (int w = 0; w < C::WORDS; ++w) {
-            scales_to_tmem(tmem_base + C::SFA_COL + w * 4, scale_desc(sfa + w * 512));
+            for (int w = 0; w < C::WORDS; ++w) {
+              scales_to_tmem<C::PAIR>(tmem_base + C::SFA_COL + w * 4, sfa + w * 32);
 #pragma unroll
-            for (int b = 0; b < C::BBLK; ++b)
-              scales_to_tmem(tmem_base + C::SFB_COL + (w * C::BBLK + b) * 4, scale_desc(sfb + (w * C::BBLK + b) * 512));
+              for (int b = 0; b < C::BBLK; ++b)
+                scales_to_tmem<C::PAIR>(tmem_base + C::SFB_COL + (w * C::BBLK + b) * 4, sfb + b * (C::SF_BLOCK >> 4) + w * 32);
+            }
+            const int steps = min(C::BK / C::UK, (a.k - kb * C::BK + C::UK - 1) / C::UK);
+#pragma unroll
+            for (int kk = 0; kk < C::BK / C::UK; ++kk) {
+              if (kk < steps) {
+                const int w = C::NV ? kk : kk >> 1;
+                constexpr uint32_t even = micro_idesc(C::NV, C::BM, 0, 0);
+                constexpr uint32_t odd = micro_idesc(C::NV, C::BM, 0, 2);
+                umma_micro<C::NV, C::PAIR>(d_tmem, desc0.a + off + kk * 2, desc0.b + off + kk * 2,
+                                           (C::NV || (kk & 1) == 0 ? even : odd) | n_bits, tmem_base + C::SFA_COL + w * 4,
+                                           tmem_base + C::SFB_COL + w * C::BBLK * 4, (kb > 0 || kk > 0) ? 1u : 0u);
+              }
+            }
+            if constexpr (C::PAIR) {
+              umma_commit_pair(&empty[stage], 0x3);
+              if (slot_done) umma_commit_pair(&sf_empty[slot], 0x3);
+            } else {
+              umma_commit(&empty[stage]);
+              if (slot_done) umma_commit(&sf_empty[slot]);
+            }
           }
-          const int steps = min(C::BK / C::UK, (a.k - kb * C::BK + C::UK - 1) / C::UK);
-          for (int kk = 0; kk < steps; ++kk) {
-            const int w = C::NV ? kk : kk >> 1;
-            const uint32_t idesc =
-                C::NV || (kk & 1) == 0 ? micro_idesc(C::NV, C::BM, C::BN, 0) : micro_idesc(C::NV, C::BM, C::BN, 2);
-            umma_micro<C::NV>(d_tmem, smem_desc_sw128(sa + kk * 32, 16, 1024), smem_desc_sw128(sb + kk * 32, 16, 1024),
-                              idesc, tmem_base + C::SFA_COL + w * 4, tmem_base + C::SFB_COL + w * C::BBLK * 4,
-                              (kb > 0 || kk > 0) ? 1u : 0u);
+          if (slot_done && ++slot == C::SF_SLOTS) {
+            slot = 0;
+            sf_phase ^= 1u;
           }
-          umma_commit(&empty[stage]);
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit(&acc_full[acc]);
+        if (elect_one()) {
+          if constexpr (C::PAIR)
+            umma_commit_pair(&acc_full[acc], 0x3);
+          else
+            umma_commit(&acc_full[acc]);
+        }
       }
-      umma_commit(drain);
-      if (!mbar_wait(drain, 0)) report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
+      if (elect_one()) {
+        if constexpr (C::PAIR)
+          umma_commit_pair(drain, 0x1);
+        else
+          umma_commit(drain);
+        if (!mbar_wait(drain, 0)) report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
+        // a pair's epilogues have released every accumulator, so that no remote arrival
+        // reaches this CTA after it has ended
+        if (C::PAIR && tile > 0 && !mbar_wait(&acc_empty[0], static_cast<uint32_t>((tile - 1) & 1)))
+          report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
+      }
     }
   } else if (warp < 2 + C::EPI_WARPS) {
     // ------------------------------------------------ epilogue
@@ -349,8 +449,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int q = warp & 3;
     const int csel = (warp - 2) >> 2;
     int tile = 0;
-    for (int L = blockIdx.x; L < n_tiles; L += grid, ++tile) {
-      const QTile t = q_tile<C>(a, *groups, nN, L);
+    for (int L = first_tile; L < n_tiles; L += grid, ++tile) {
+      const QTile t = q_tile<C>(a, *groups, nM, L);
       const int acc = tile & 1;
       float alpha = 1.0f;
       if (a.x_scale != nullptr) alpha = __ldg(a.x_scale);
@@ -360,102 +460,191 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         break;
       }
       tc_fence_after();
-      const bool row_ok = q * 32 + lane < t.valid;
-      OutT* row = static_cast<OutT*>(a.out) + (static_cast<int64_t>(t.m0) + q * 32 + lane) * a.n + t.n0;
+      const int mrow = t.m0 + 128 * rank + q * 32;  // first output column of this warp
+      OutT* out = static_cast<OutT*>(a.out) + static_cast<int64_t>(t.n0) * a.n + mrow;
       const uint32_t tb = tmem_base + (acc ? C::ACC1 : 0u) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
       for (int i = 0; i < C::CHUNKS; ++i) {
-        // the two warps of a lane quarter take alternate 32-column chunks; the
-        // columns shared with the other accumulator come first: the upper end of
-        // the first accumulator, the lower end of the second
+        // the two warps of a lane quarter take alternate chunks of 32 rows; the
+        // accumulator columns shared with the other accumulator come first: the upper
+        // end of the first accumulator, the lower end of the second
         const int j = C::OVERLAP && acc == 0 ? C::CHUNKS - 1 - i : i;
         const int c = (2 * j + csel) * 32;
         uint32_t r[32];
-        tmem_ld32(tb + c, r);
-        tmem_ld_wait();
+        if (c < t.N) {
+          tmem_ld32(tb + c, r);
+          tmem_ld_wait();
+        }
         if (i == (C::OVERLAP ? 0 : C::CHUNKS - 1)) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[C::OVERLAP ? 0 : acc]);
+          if (lane == 0) {
+            if constexpr (C::PAIR)
+              mbar_arrive_cluster(acc_empty_leader);
+            else
+              mbar_arrive(&acc_empty[C::OVERLAP ? 0 : acc]);
+          }
         }
-        if (row_ok) store_row32<OutT>(row + c, r, alpha, a.n - t.n0 - c);
+        if (c < t.N) {
+          float v[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]) * alpha;
+          store_chunk_turned<OutT>(v, out + static_cast<int64_t>(c) * a.n, a.n, t.left - c, a.n - mrow, lane);
+        }
       }
     }
   } else {
-    // ------------------------------------------------ scale loaders: warp 0 of these
-    // the rows of A, the others a 128-row block of B each
+    // ------------------------------------------------ scale warps: warp 0 of these the
+    // rows of A, then a 128-row block of B each, the last the TMA producer
     const int who = warp - 2 - C::EPI_WARPS;
-    const int row_bytes = a.k / (C::NV ? 16 : 32);
-    const bool whole = a.k % C::BK == 0;
-    const uint32_t dst = (who == 0 ? C::A_BYTES + C::B_BYTES : C::A_BYTES + C::B_BYTES + C::SFA_BYTES + (who - 1) * 512);
-    const int word_step = who == 0 ? 512 : 512 * C::BBLK;
-    // the load side runs AHEAD stages before the store side
-    int lL = blockIdx.x, lkb = 0;
-    const uint8_t* src[4];
-    bool live[4];
-    auto aim = [&]() {
-      if (lL >= n_tiles) return;
-      const QTile t = q_tile<C>(a, *groups, nN, lL);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane + 32 * i;
-        if (who == 0) {
-          live[i] = r < t.valid;
-          src[i] = a.xs + (static_cast<int64_t>(t.m0) + r) * row_bytes;
-        } else {
-          const int n = t.n0 + (who - 1) * 128 + r;
-          live[i] = n < a.n && (C::BN >= 128 || r < C::BN);
-          src[i] = a.ws + (static_cast<int64_t>(t.e) * a.n + n) * row_bytes;
-        }
-      }
-    };
-    aim();
-    uint32_t buf[C::AHEAD][4][C::WORDS];
-    auto fetch = [&](uint32_t (&b)[4][C::WORDS]) {
-      if (lL >= n_tiles) return;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (live[i]) {
-          load_scale_words<C::WORDS>(b[i], src[i], lkb * C::SCALE_BYTES, row_bytes, whole);
-        } else {
-#pragma unroll
-          for (int w = 0; w < C::WORDS; ++w) b[i][w] = 0u;
-        }
-      }
-      if (++lkb == nk) {
-        lkb = 0;
-        lL += grid;
-        aim();
-      }
-    };
-#pragma unroll
-    for (int s = 0; s < C::AHEAD; ++s) fetch(buf[s]);
-    const int my_tiles = blockIdx.x < n_tiles ? (n_tiles - 1 - static_cast<int>(blockIdx.x)) / grid + 1 : 0;
-    const int64_t total = static_cast<int64_t>(my_tiles) * nk;
-    int stage = 0;
+    const int my_tiles = first_tile < n_tiles ? (n_tiles - 1 - first_tile) / grid + 1 : 0;
+    unsigned char* const block0 = sf_base + who * C::SF_BLOCK;
+    int slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    for (int64_t it = 0; it < total && ok; it += C::AHEAD) {
+    auto step = [&]() {
+      if (++slot == C::SF_SLOTS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    };
+    // writes the lines of a slot's block, this lane's rows being lane + 32 i: the tensor
+    // core may read them
+    auto hand_over = [&](const uint32_t (&r)[4][8]) {
+      uint4* block = reinterpret_cast<uint4*>(block0 + static_cast<size_t>(slot) * C::SF_BYTES);
 #pragma unroll
-      for (int s = 0; s < C::AHEAD; ++s) {
-        if (it + s < total && ok) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u))) {
-            if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
-            ok = false;
-          } else {
-            unsigned char* line = smem + static_cast<size_t>(stage) * C::STAGE_BYTES + dst + lane * 16;
-#pragma unroll
-            for (int w = 0; w < C::WORDS; ++w)
-              *reinterpret_cast<uint4*>(line + w * word_step) =
-                  make_uint4(buf[s][0][w], buf[s][1][w], buf[s][2][w], buf[s][3][w]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[stage]);
-            if (++stage == C::STAGES) {
-              stage = 0;
-              phase ^= 1u;
+      for (int w = 0; w < 8; ++w) block[lane + 32 * w] = make_uint4(r[0][w], r[1][w], r[2][w], r[3][w]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (C::PAIR)
+          mbar_arrive_cluster(sf_full_leader + static_cast<uint32_t>(slot * sizeof(uint64_t)));
+        else
+          mbar_arrive(&sf_full[slot]);
+      }
+      step();
+    };
+    const int slots = (nk + C::SF_STAGES_PER - 1) / C::SF_STAGES_PER;  // of a tile
+    if (who == C::SF_WARPS) {
+      if (a.tma_scales) {
+        int issued = 0;
+        bool ok = true;
+        for (int L = first_tile; L < n_tiles && ok; L += grid) {
+          const QTile t = q_tile<C>(a, *groups, nM, L);
+          const int rows = uniform(t.N);
+          const int boxes = rows > C::BN - 32 ? 0 : (rows + 31) / 32;
+          const uint32_t bytes = static_cast<uint32_t>(32 * (128 + (boxes == 0 ? C::BN : 32 * boxes)));
+          const int row = uniform(t.n0);
+          const int col = uniform(t.m0) + 128 * rank;
+          const int e = uniform(t.e);
+          for (int j = 0; j < slots; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase ^ 1u))) {
+              if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
+              ok = false;
+              break;
             }
-            fetch(buf[s]);
+            if (elect_one()) {
+              unsigned char* sf = sf_base + static_cast<size_t>(slot) * C::SF_BYTES;
+              mbar_arrive_expect_tx(&sf_raw[slot], bytes);
+              tma_load_3d(&tmSA, &sf_raw[slot], sf, j * 32, col, e);
+              if (boxes == 0) {
+                tma_load_3d(&tmSB, &sf_raw[slot], sf + C::SF_BLOCK, j * 32, row, 0);
+              } else {
+                for (int q = 0; q < boxes; ++q)
+                  tma_load_3d(&tmSB32, &sf_raw[slot], sf + C::SF_BLOCK + q * 1024, j * 32, row + 32 * q, 0);
+              }
+            }
+            ++issued;
+            step();
+          }
+        }
+        for (int s = 0; s < C::SF_SLOTS && s < issued; ++s) {
+          const int last = (issued - 1 - s) / C::SF_SLOTS;
+          if (!mbar_wait(&sf_raw[s], static_cast<uint32_t>(last & 1))) report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
+        }
+      }
+    } else if (a.tma_scales) {
+      for (int i = 0; i < my_tiles * slots; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[slot], phase))) {
+          if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
+          break;
+        }
+        const uint4* raw = reinterpret_cast<const uint4*>(block0 + static_cast<size_t>(slot) * C::SF_BYTES);
+        uint32_t r[4][8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = lane + 32 * q;
+          const int flip = (row >> 2) & 1;  // 32-byte swizzle: which 16-byte half comes first
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = raw[2 * row + (h ^ flip)];
+            r[q][4 * h] = v.x;
+            r[q][4 * h + 1] = v.y;
+            r[q][4 * h + 2] = v.z;
+            r[q][4 * h + 3] = v.w;
+          }
+        }
+        __syncwarp();
+        hand_over(r);
+      }
+    } else {
+      // through registers, AHEAD slots at a time
+      const int row_bytes = a.k / (C::NV ? 16 : 32);
+      const uint8_t* end = who == 0 ? a.ws + static_cast<int64_t>(a.E) * a.n * row_bytes : a.xs + a.rows * row_bytes;
+      int lL = first_tile, lj = 0;
+      const uint8_t* src[4];
+      bool live[4];
+      auto aim = [&]() {
+        if (lL >= n_tiles) return;
+        const QTile t = q_tile<C>(a, *groups, nM, lL);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i;
+          if (who == 0) {
+            const int m = t.m0 + 128 * rank + r;
+            live[i] = m < a.n;
+            src[i] = a.ws + (static_cast<int64_t>(t.e) * a.n + m) * row_bytes;
+          } else {
+            const int x = (who - 1) * 128 + r;
+            live[i] = x < t.left;
+            src[i] = a.xs + (static_cast<int64_t>(t.n0) + x) * row_bytes;
+          }
+        }
+      };
+      aim();
+      uint32_t buf[C::AHEAD][4][8];
+      auto fetch = [&](uint32_t (&b)[4][8]) {
+        if (lL >= n_tiles) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (live[i]) {
+            load_scale_words<8>(b[i], src[i], lj * 32, row_bytes, end);
+          } else {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) b[i][w] = 0u;
+          }
+        }
+        if (++lj == slots) {
+          lj = 0;
+          lL += grid;
+          aim();
+        }
+      };
+      const int total = my_tiles * slots;
+      bool ok = true;
+      for (int it = 0; it < total && ok; it += C::AHEAD) {
+        // all loads of a batch, then their stores: the fence in hand_over waits for
+        // whatever the warp has in flight
+#pragma unroll
+        for (int s = 0; s < C::AHEAD; ++s) fetch(buf[s]);
+#pragma unroll
+        for (int s = 0; s < C::AHEAD; ++s) {
+          if (it + s < total && ok) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase ^ 1u))) {
+              if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
+              ok = false;
+            } else {
+              hand_over(buf[s]);
+            }
           }
         }
       }
@@ -465,39 +654,60 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (C::PAIR) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if constexpr (C::PAIR)
+      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
 }
 
 // -------------------------------------------------------------- host side
 
 template <class C>
-cudaError_t launch_q(const void* x, const void* w, const QArgs& a, int64_t max_tiles, cudaStream_t st) {
+cudaError_t launch_q(const void* x, const void* w, const QArgs& a, cudaStream_t st) {
   static std::atomic<size_t> smem_set[kMaxDevices];
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(microscaled_gemm_kernel<C>), C::SMEM_BYTES, smem_set);
   if (e != cudaSuccess) return e;
   const uint64_t row_bytes = static_cast<uint64_t>(a.k) / 2;
-  CUtensorMap ta, ta32, tb;
-  if (!make_map_bytes(&ta, x, 1, static_cast<uint64_t>(a.rows), row_bytes, 128) ||
-      !make_map_bytes(&ta32, x, 1, static_cast<uint64_t>(a.rows), row_bytes, 32) ||
-      !make_map_bytes(&tb, w, static_cast<uint64_t>(a.E), static_cast<uint64_t>(a.n), row_bytes, C::BN))
+  const uint64_t rows = static_cast<uint64_t>(a.rows), n = static_cast<uint64_t>(a.n), E = static_cast<uint64_t>(a.E);
+  CUtensorMap ta, tb, tb32;
+  if (!make_map_bytes(&ta, w, E, n, row_bytes, 128) || !make_map_bytes(&tb, x, 1, rows, row_bytes, C::B_ROWS) ||
+      !make_map_bytes(&tb32, x, 1, rows, row_bytes, 32))
     return cudaErrorInvalidValue;
-  const int64_t sms = device_sm_count();
-  const unsigned grid = static_cast<unsigned>(max_tiles < sms ? max_tiles : sms);
-  return launch_dependent(microscaled_gemm_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, nullptr, 0, ta,
-                          ta32, tb, a);
+  CUtensorMap tsa = ta, tsb = tb, tsb32 = tb32;
+  if (a.tma_scales) {
+    const uint64_t sf_bytes = static_cast<uint64_t>(a.k) / (C::NV ? 16 : 32);
+    if (!make_map_scales(&tsa, a.ws, E, n, sf_bytes, 128) || !make_map_scales(&tsb, a.xs, 1, rows, sf_bytes, C::BN) ||
+        !make_map_scales(&tsb32, a.xs, 1, rows, sf_bytes, 32))
+      return cudaErrorInvalidValue;
+  }
+  // row tiles: at most one more than full ones for every group that has rows
+  const int64_t tiles = (a.rows / C::BN + (a.rows < a.E ? a.rows : a.E)) * ((a.n + C::BM - 1) / C::BM);
+  const int64_t most = device_sm_count() / C::CTAS;
+  const unsigned units = static_cast<unsigned>(tiles < most ? tiles : most);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  return launch_dependent(microscaled_gemm_kernel<C>, dim3(C::CTAS * units), dim3(C::THREADS), C::SMEM_BYTES, st, attr,
+                          C::PAIR ? 1 : 0, ta, tb, tb32, tsa, tsb, tsb32, a);
 }
 
 template <bool NV, bool O32>
-cudaError_t run_q(const void* x, const void* w, const QArgs& a, cudaStream_t st) {
-  const int64_t row_tiles = a.rows / 128 + (a.rows < a.E ? a.rows : a.E);
-  const int bn = pick_tile_width(row_tiles, a.n);
-  const int64_t max_tiles = row_tiles * ((a.n + bn - 1) / bn);
-  if (bn == 256) return launch_q<QCfg<NV, 256, O32>>(x, w, a, max_tiles, st);
-  if (bn == 128) return launch_q<QCfg<NV, 128, O32>>(x, w, a, max_tiles, st);
-  return launch_q<QCfg<NV, 64, O32>>(x, w, a, max_tiles, st);
+cudaError_t run_q(const void* x, const void* w, QArgs& a, cudaStream_t st) {
+  a.tma_scales = a.k / (NV ? 16 : 32) % 16 == 0;
+  // a stage of 256 terms takes about 1.75 times one of 64 bf16 terms
+  switch (pick_row_tile(a.rows, a.E, a.n, (a.k + 255) / 256, 175)) {
+    case kTilePair: return launch_q<QCfg<NV, 256, O32, true>>(x, w, a, st);
+    case kTile256: return launch_q<QCfg<NV, 256, O32, false>>(x, w, a, st);
+    case kTile128: return launch_q<QCfg<NV, 128, O32, false>>(x, w, a, st);
+    case kTile64: return launch_q<QCfg<NV, 64, O32, false>>(x, w, a, st);
+    default: return launch_q<QCfg<NV, 32, O32, false>>(x, w, a, st);
+  }
 }
 
 }  // namespace
@@ -506,7 +716,7 @@ cudaError_t launch_ragged_microscaled(bool nv, int64_t rows, int E, int n, int k
                                       const uint8_t* xs, const float* xg, const int32_t* gs, const int32_t* off,
                                       const uint8_t* wc, const uint8_t* ws, const float* wg, void* y, int32_t* status,
                                       cudaStream_t st) {
-  const QArgs a{gs, off, xs, ws, xg, wg, rows, E, n, k, y, status};
+  QArgs a{gs, off, xs, ws, xg, wg, rows, E, n, k, false, y, status};
   if (nv) return out32 ? run_q<true, true>(xc, wc, a, st) : run_q<true, false>(xc, wc, a, st);
   return out32 ? run_q<false, true>(xc, wc, a, st) : run_q<false, false>(xc, wc, a, st);
 }

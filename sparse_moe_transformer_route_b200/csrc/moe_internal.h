@@ -194,6 +194,9 @@ bool make_map_3d(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows,
                  uint32_t box_rows);
 bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows, uint64_t row_bytes,
                     uint32_t box_rows);
+// Boxes 32 bytes wide, 32-byte swizzle, over rows of block scales [mats, rows, row_bytes].
+bool make_map_scales(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows, uint64_t row_bytes,
+                     uint32_t box_rows);
 
 // Ragged products grouped by expert (ragged_gemm.cu): y = W_e x, dx = W_e^T dy,
 // dW_e = sum dy x^T over rows [start_e, start_e + count_e) of buffers of `rows` rows.
@@ -203,8 +206,12 @@ cudaError_t launch_ragged_dgrad(int64_t rows, int E, int n, int k, bool out32, c
                                 const int32_t* off, const void* w, void* dx, int32_t* status, cudaStream_t st);
 cudaError_t launch_ragged_wgrad(int64_t rows, int E, int n, int k, bool out32, const void* dy, const void* x,
                                 const int32_t* gs, const int32_t* off, void* dw, int32_t* status, cudaStream_t st);
-// Columns of an output tile (256, 128 or 64) for `row_tiles` 128-row tiles.
-int pick_tile_width(int64_t row_tiles, int cols);
+// Kinds of tiles: at most 32, 64, 128 or 256 rows of a group by 128 output columns on one
+// CTA, or 256 by 256 on a pair of CTAs.
+enum TileKind { kTile32, kTile64, kTile128, kTile256, kTilePair, kTileKinds };
+// The kind for `rows` rows in E groups, `out_cols` output columns and a reduction of
+// `stages` stages, one of which takes stage_percent of a 64-term stage of bf16.
+int pick_row_tile(int64_t rows, int E, int out_cols, int64_t stages, int stage_percent);
 // The same product on 4-bit operands (microscaled_gemm.cu).
 cudaError_t launch_ragged_microscaled(bool nv, int64_t rows, int E, int n, int k, bool out32, const uint8_t* xc,
                                       const uint8_t* xs, const float* xg, const int32_t* gs, const int32_t* off,

@@ -1,5 +1,5 @@
 // Shared by the ragged grouped products: the checked group layout in shared memory,
-// the tile schedule, and the masked store of an accumulator chunk.
+// the tile schedule, the issue of MMAs, and the masked stores of an accumulator chunk.
 #pragma once
 
 #include <type_traits>
@@ -9,20 +9,31 @@
 
 namespace moe {
 
-// Expert e owns `count[e]` rows from `start[e]` on. `tiles[e]` is the first row tile
-// of expert e and `tiles[E]` their number.
+// Expert e owns `count[e]` rows from `start[e]` on, cut into row tiles, each with the
+// same number of column tiles. Experts come in the order `order[0..E)`; `tiles[j]` is the
+// number of the j-th one's first tile and `tiles[E]` their sum.
 struct RaggedGroups {
   int32_t start[kMaxExperts];
   int32_t count[kMaxExperts];
+  int32_t order[kMaxExperts];
   int32_t tiles[kMaxExperts + 1];
 };
 
+// A group's row tiles: as few as tiles of at most MOST rows allow, all of one size, a
+// multiple of UNIT, but the last.
+template <int MOST, int UNIT>
+__device__ __forceinline__ int rows_a_tile(int count) {
+  const int least = max(1, (count + MOST - 1) / MOST);
+  return min(MOST, max(UNIT, ((count + least - 1) / least + UNIT - 1) / UNIT * UNIT));
+}
+
 // Reads the layout (all threads of the CTA; it ends with a block barrier). A group
 // that does not lie inside [0, rows) is recorded and treated as empty, so that no
-// later access depends on a bad offset. TILE_ROWS: rows a tile.
-template <int TILE_ROWS>
-__device__ __forceinline__ void load_groups(RaggedGroups* g, const int32_t* group_start, const int32_t* offsets,
-                                            int E, int64_t rows, int32_t* status) {
+// later access depends on a bad offset. cols: column tiles of a row tile. SORTED: the
+// experts come by falling row count (equal counts in order of e).
+template <int MOST, int UNIT, bool SORTED>
+__device__ __forceinline__ void load_groups(RaggedGroups* g, const int32_t* group_start, const int32_t* offsets, int E,
+                                            int64_t rows, int cols, int32_t* status) {
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     const int64_t lo = offsets[e], hi = offsets[e + 1];
     const int64_t s = group_start != nullptr ? group_start[e] : lo;
@@ -33,34 +44,50 @@ __device__ __forceinline__ void load_groups(RaggedGroups* g, const int32_t* grou
     }
     g->start[e] = c > 0 ? static_cast<int32_t>(s) : 0;
     g->count[e] = static_cast<int32_t>(c);
+    if constexpr (!SORTED) g->order[e] = e;
   }
   __syncthreads();
+  if constexpr (SORTED) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      int rank = 0;
+      const int mine = g->count[e];
+      for (int o = 0; o < E; ++o) rank += g->count[o] > mine || (g->count[o] == mine && o < e);
+      g->order[rank] = e;
+    }
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {  // one warp: a prefix sum over 32 experts a turn
+    const int lane = static_cast<int>(threadIdx.x);
     int carry = 0;
     for (int base = 0; base < E; base += 32) {
-      const int e = base + static_cast<int>(threadIdx.x);
-      const int mine = e < E ? (g->count[e] + TILE_ROWS - 1) / TILE_ROWS : 0;
+      const int j = base + lane;
+      int mine = 0;
+      if (j < E) {
+        const int c = g->count[g->order[j]];
+        const int per = rows_a_tile<MOST, UNIT>(c);
+        mine = (c + per - 1) / per * cols;
+      }
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (static_cast<int>(threadIdx.x) >= o) incl += up;
+        if (lane >= o) incl += up;
       }
-      if (e < E) g->tiles[e] = carry + incl - mine;
+      if (j < E) g->tiles[j] = carry + incl - mine;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (threadIdx.x == 0) g->tiles[E] = carry;
+    if (lane == 0) g->tiles[E] = carry;
   }
   __syncthreads();
 }
 
-// The expert of row tile `mt`: the largest e with tiles[e] <= mt (an expert without
-// rows owns no tile and is never found).
-__device__ __forceinline__ int tile_expert(const RaggedGroups& g, int E, int mt) {
+// The place in `order` of the expert of tile L: the largest j with tiles[j] <= L (an
+// expert without rows owns no tile and is never found).
+__device__ __forceinline__ int tile_place(const RaggedGroups& g, int E, int L) {
   int lo = 0, hi = E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (g.tiles[mid] <= mt) lo = mid; else hi = mid - 1;
+    if (g.tiles[mid] <= L) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
@@ -142,7 +169,7 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       : "memory");
 }
 
-// The same by a CTA of a pair, its bytes counted on the leader's barrier (see tma_load_2d_pair).
+// tma_load_3d by a CTA of a pair, its bytes counted on the leader's barrier (see tma_load_2d_pair).
 __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t c0,
                                                  int32_t c1, int32_t c2) {
   asm volatile(
@@ -152,33 +179,33 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint64_
       : "memory");
 }
 
-// Arrival on another CTA's barrier that orders this thread's earlier writes for whoever
-// waits there with cluster scope.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-// mbar_wait whose completion orders what the arrivals of both CTAs released.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  uint32_t spins = 0;
-  while (!mbar_try_wait_cluster(bar, parity)) {
-    if (((++spins) & 255u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) return false;
+// One warp writes a 32 x 32 chunk whose COLUMN `lane` this thread holds in v: v[j] is
+// the element of row j. fp32 rows leave as 128 bytes a store; bf16 neighbours swap one
+// of every two rows, and two rows of 64 bytes leave a store. Only the first `rows` rows
+// and `cols` columns (a multiple of 8) are written.
+template <typename T>
+__device__ __forceinline__ void store_chunk_turned(const float (&v)[32], T* g, int64_t ld, int rows, int cols,
+                                                   int lane) {
+  if constexpr (std::is_same_v<T, float>) {
+    float* p = g + lane;
+    if (lane >= cols) rows = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < rows) *p = v[j];
+      p += ld;
+    }
+  } else {
+    const bool odd = (lane & 1) != 0;
+    T* p = g + (lane & ~1) + (odd ? ld : 0);
+    const int mine = lane < cols ? rows - (odd ? 1 : 0) : 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+      const uint32_t w = odd ? pack_bf16x2(other, v[j + 1]) : pack_bf16x2(v[j], other);
+      if (j < mine) *reinterpret_cast<uint32_t*>(p) = w;
+      p += 2 * ld;
+    }
   }
-  return true;
 }
 
 // One warp writes a 32 x 32 chunk whose row `lane` this thread holds in v, through
@@ -188,7 +215,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 template <typename T, int PITCH>
 __device__ __forceinline__ void store_chunk_masked(unsigned char* stg, const float (&v)[32], T* g, int64_t ld, int rows,
                                                    int cols, int lane) {
-  constexpr int CPP = ((PITCH - 16) / static_cast<int>(sizeof(T))) < 32 ? 16 : 32;  // columns a pass
+  constexpr int CPP = (PITCH - 16) / static_cast<int>(sizeof(T));  // columns a pass
+  static_assert(CPP == 32 || CPP == 16 || CPP == 8, "pitch");
   constexpr int RB = CPP * static_cast<int>(sizeof(T));
   constexpr int LPR = RB / 16;   // lanes a row on the way out
   constexpr int RPI = 32 / LPR;  // rows a store instruction
