@@ -514,12 +514,28 @@ def moe_stack_forward(cfg, layers, resid, ws, stream=None):
 # ---------------------------------------------------------------- ragged products, 4-bit values
 
 
-def _one_device(*tensors):
-    """The tensors lie on the current device, the one the call launches on."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensors must be on the current device (cuda:{cur}), got {t.device}")
+def _arg(t, dtype, shape, name, device, allow_none=False):
+    """The address of a contiguous tensor of this type and shape on the current device, the
+    one the call launches on. One pass over what a right argument satisfies (a call of
+    these takes up to ten tensors and a few microseconds); a wrong one is told by _ptr."""
+    if t is None and allow_none:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == device):
+        return t.data_ptr()
+    _ptr(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
+
+
+def _current_device():
+    """The current device, or -2 (no tensor's) before CUDA is used at all."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)  # current_stream() builds an object: 2 us
 
 
 def grouped_shape(rows, n_experts, n, k, out_dtype=torch.bfloat16):
@@ -547,46 +563,45 @@ def _out_dtype(shape):
     return torch.bfloat16 if shape.out_dtype == MOE_BF16 else torch.float32
 
 
-def _group_ptrs(shape, group_start, offsets):
-    E = shape.n_experts
-    return (_ptr(group_start, torch.int32, (E + 1,), "group_start", allow_none=True),
-            _ptr(offsets, torch.int32, (E + 1,), "offsets"))
+def _group_args(shape, group_start, offsets, dev):
+    E = (shape.n_experts + 1,)
+    return (_arg(group_start, torch.int32, E, "group_start", dev, allow_none=True),
+            _arg(offsets, torch.int32, E, "offsets", dev))
+
+
+def _workspace_arg(ws, dev):
+    return _arg(ws, torch.uint8, ws.shape if isinstance(ws, torch.Tensor) else None, "ws", dev)
 
 
 def moe_grouped_gemm(shape, x, group_start, offsets, w, y, ws, stream=None):
     """y[r] = W_e x[r] for the rows r of expert e: rows [group_start[e], + count_e), or
     [offsets[e], offsets[e+1]) when group_start is None."""
-    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
-    gs, off = _group_ptrs(shape, group_start, offsets)
-    px, pw = _ptr(x, torch.bfloat16, (R, k), "x"), _ptr(w, torch.bfloat16, (E, n, k), "w")
-    py = _ptr(y, _out_dtype(shape), (R, n), "y")
-    pws = _ptr(ws, torch.uint8, name="ws")
-    _one_device(x, group_start, offsets, w, y, ws)
-    st = lib().moe_grouped_gemm(ctypes.byref(shape), px, gs, off, pw, py, pws, ws.numel(), _stream(stream))
+    R, E, n, k, dev, bf = shape.rows, shape.n_experts, shape.n, shape.k, _current_device(), torch.bfloat16
+    gs, off = _group_args(shape, group_start, offsets, dev)
+    st = lib().moe_grouped_gemm(ctypes.byref(shape), _arg(x, bf, (R, k), "x", dev), gs, off,
+                                _arg(w, bf, (E, n, k), "w", dev), _arg(y, _out_dtype(shape), (R, n), "y", dev),
+                                _workspace_arg(ws, dev), ws.numel(), _raw_stream(stream, dev))
     _check(st, "moe_grouped_gemm")
 
 
 def moe_grouped_gemm_dgrad(shape, dy, group_start, offsets, w, dx, ws, stream=None):
     """dx[r] = W_e^T dy[r]: the gradient of moe_grouped_gemm with respect to x."""
-    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
-    gs, off = _group_ptrs(shape, group_start, offsets)
-    pdy, pw = _ptr(dy, torch.bfloat16, (R, n), "dy"), _ptr(w, torch.bfloat16, (E, n, k), "w")
-    pdx = _ptr(dx, _out_dtype(shape), (R, k), "dx")
-    pws = _ptr(ws, torch.uint8, name="ws")
-    _one_device(dy, group_start, offsets, w, dx, ws)
-    st = lib().moe_grouped_gemm_dgrad(ctypes.byref(shape), pdy, gs, off, pw, pdx, pws, ws.numel(), _stream(stream))
+    R, E, n, k, dev, bf = shape.rows, shape.n_experts, shape.n, shape.k, _current_device(), torch.bfloat16
+    gs, off = _group_args(shape, group_start, offsets, dev)
+    st = lib().moe_grouped_gemm_dgrad(ctypes.byref(shape), _arg(dy, bf, (R, n), "dy", dev), gs, off,
+                                      _arg(w, bf, (E, n, k), "w", dev), _arg(dx, _out_dtype(shape), (R, k), "dx", dev),
+                                      _workspace_arg(ws, dev), ws.numel(), _raw_stream(stream, dev))
     _check(st, "moe_grouped_gemm_dgrad")
 
 
 def moe_grouped_gemm_wgrad(shape, dy, x, group_start, offsets, dw, ws, stream=None):
     """dW_e = sum over the rows r of e of dy[r] x[r]^T (zero without rows)."""
-    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
-    gs, off = _group_ptrs(shape, group_start, offsets)
-    pdy, px = _ptr(dy, torch.bfloat16, (R, n), "dy"), _ptr(x, torch.bfloat16, (R, k), "x")
-    pdw = _ptr(dw, _out_dtype(shape), (E, n, k), "dw")
-    pws = _ptr(ws, torch.uint8, name="ws")
-    _one_device(dy, x, group_start, offsets, dw, ws)
-    st = lib().moe_grouped_gemm_wgrad(ctypes.byref(shape), pdy, px, gs, off, pdw, pws, ws.numel(), _stream(stream))
+    R, E, n, k, dev, bf = shape.rows, shape.n_experts, shape.n, shape.k, _current_device(), torch.bfloat16
+    gs, off = _group_args(shape, group_start, offsets, dev)
+    st = lib().moe_grouped_gemm_wgrad(ctypes.byref(shape), _arg(dy, bf, (R, n), "dy", dev),
+                                      _arg(x, bf, (R, k), "x", dev), gs, off,
+                                      _arg(dw, _out_dtype(shape), (E, n, k), "dw", dev), _workspace_arg(ws, dev),
+                                      ws.numel(), _raw_stream(stream, dev))
     _check(st, "moe_grouped_gemm_wgrad")
 
 
@@ -597,55 +612,54 @@ def _micro_block(fmt):
 
 
 def _micro_shape(t, name):
-    """[groups, rows, cols] of a matrix or a stack of matrices."""
+    """[groups, rows, cols] of a matrix or a stack of matrices, and its dtype code."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() not in (2, 3):
         raise ValueError(f"{name} must have two or three dimensions")
     if t.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+    return (1, *t.shape, int(t.dtype is torch.float32)) if t.dim() == 2 else (*t.shape, int(t.dtype is torch.float32))
 
 
-def _micro_ptrs(fmt, t, name, tensor_scale, codes, scales):
-    """Shape, dtype code and pointers of a conversion between `t` and its 4-bit form."""
+def _micro_args(fmt, t, name, tensor_scale, codes, scales, dev):
+    """Shape, dtype code and addresses of a conversion between `t` and its 4-bit form."""
     block = _micro_block(fmt)
-    G, R, K = _micro_shape(t, name)
+    G, R, K, dt = _micro_shape(t, name)
     if K % 32:
         raise ValueError(f"{name} must have a multiple of 32 columns, got {K}")
-    lead = tuple(t.shape[:-1])
-    pt = _ptr(t, None, None, name)
-    pc = _ptr(codes, torch.uint8, (*lead, K // 2), "codes")
-    ps = _ptr(scales, torch.uint8, (*lead, K // block), "scales")
-    pg = _ptr(tensor_scale, torch.float32, (G,), "tensor_scale", allow_none=True)
-    _one_device(t, tensor_scale, codes, scales)
-    return G, R, K, MOE_BF16 if t.dtype == torch.bfloat16 else MOE_FP32, pt, pg, pc, ps
+    lead = t.shape[:-1]
+    return (G, R, K, dt, _arg(t, t.dtype, t.shape, name, dev),
+            _arg(tensor_scale, torch.float32, (G,), "tensor_scale", dev, allow_none=True),
+            _arg(codes, torch.uint8, (*lead, K // 2), "codes", dev),
+            _arg(scales, torch.uint8, (*lead, K // block), "scales", dev))
 
 
 def moe_tensor_scale_microscaled(x, scale, stream=None):
     """scale[g] = max(amax of x[g] / 2688, 2^-100), the tensor scale MOE_NVFP4 blocks are
     scaled against. x: [groups, rows, cols], or [rows, cols] as one group."""
-    G, R, K = _micro_shape(x, "x")
-    px, pg = _ptr(x, None, None, "x"), _ptr(scale, torch.float32, (G,), "scale")
-    _one_device(x, scale)
-    st = lib().moe_tensor_scale_microscaled(G, R, K, MOE_BF16 if x.dtype == torch.bfloat16 else MOE_FP32, px, pg,
-                                            _stream(stream))
+    dev = _current_device()
+    G, R, K, dt = _micro_shape(x, "x")
+    st = lib().moe_tensor_scale_microscaled(G, R, K, dt, _arg(x, x.dtype, x.shape, "x", dev),
+                                            _arg(scale, torch.float32, (G,), "scale", dev), _raw_stream(stream, dev))
     _check(st, "moe_tensor_scale_microscaled")
 
 
 def moe_quantize_microscaled(fmt, x, tensor_scale, codes, scales, stream=None):
     """x [groups, rows, cols] (or [rows, cols]) to 4-bit codes [.., cols / 2] and block
     scales [.., cols / 32] (MOE_MXFP4) or [.., cols / 16] (MOE_NVFP4), uint8."""
-    G, R, K, dt, px, pg, pc, ps = _micro_ptrs(fmt, x, "x", tensor_scale, codes, scales)
-    st = lib().moe_quantize_microscaled(fmt, G, R, K, dt, px, pg, pc, ps, _stream(stream))
+    dev = _current_device()
+    G, R, K, dt, px, pg, pc, ps = _micro_args(fmt, x, "x", tensor_scale, codes, scales, dev)
+    st = lib().moe_quantize_microscaled(fmt, G, R, K, dt, px, pg, pc, ps, _raw_stream(stream, dev))
     _check(st, "moe_quantize_microscaled")
 
 
 def moe_dequantize_microscaled(fmt, codes, scales, tensor_scale, out, stream=None):
     """The values that codes and scales stand for, into out [groups, rows, cols] (or
     [rows, cols]), bf16 or fp32."""
-    G, R, K, dt, po, pg, pc, ps = _micro_ptrs(fmt, out, "out", tensor_scale, codes, scales)
-    st = lib().moe_dequantize_microscaled(fmt, G, R, K, dt, pc, ps, pg, po, _stream(stream))
+    dev = _current_device()
+    G, R, K, dt, po, pg, pc, ps = _micro_args(fmt, out, "out", tensor_scale, codes, scales, dev)
+    st = lib().moe_dequantize_microscaled(fmt, G, R, K, dt, pc, ps, pg, po, _raw_stream(stream, dev))
     _check(st, "moe_dequantize_microscaled")
 
 
@@ -653,19 +667,16 @@ def moe_grouped_gemm_microscaled(shape, fmt, x_codes, x_scales, x_scale, group_s
                                  w_scale, y, ws, stream=None):
     """moe_grouped_gemm on 4-bit rows and weights of one format; x_scale [1] and
     w_scale [n_experts] are the tensor scales of MOE_NVFP4 operands (None: 1)."""
-    R, E, n, k = shape.rows, shape.n_experts, shape.n, shape.k
+    R, E, n, k, dev, u8 = shape.rows, shape.n_experts, shape.n, shape.k, _current_device(), torch.uint8
     block = _micro_block(fmt)
-    gs, off = _group_ptrs(shape, group_start, offsets)
-    pxc, pxs = _ptr(x_codes, torch.uint8, (R, k // 2), "x_codes"), _ptr(x_scales, torch.uint8, (R, k // block), "x_scales")
-    pwc = _ptr(w_codes, torch.uint8, (E, n, k // 2), "w_codes")
-    pws_ = _ptr(w_scales, torch.uint8, (E, n, k // block), "w_scales")
-    pxg = _ptr(x_scale, torch.float32, (1,), "x_scale", allow_none=True)
-    pwg = _ptr(w_scale, torch.float32, (E,), "w_scale", allow_none=True)
-    py = _ptr(y, _out_dtype(shape), (R, n), "y")
-    pws = _ptr(ws, torch.uint8, name="ws")
-    _one_device(x_codes, x_scales, x_scale, group_start, offsets, w_codes, w_scales, w_scale, y, ws)
-    st = lib().moe_grouped_gemm_microscaled(ctypes.byref(shape), fmt, pxc, pxs, pxg, gs, off, pwc, pws_, pwg, py, pws,
-                                            ws.numel(), _stream(stream))
+    gs, off = _group_args(shape, group_start, offsets, dev)
+    st = lib().moe_grouped_gemm_microscaled(
+        ctypes.byref(shape), fmt, _arg(x_codes, u8, (R, k // 2), "x_codes", dev),
+        _arg(x_scales, u8, (R, k // block), "x_scales", dev),
+        _arg(x_scale, torch.float32, (1,), "x_scale", dev, allow_none=True), gs, off,
+        _arg(w_codes, u8, (E, n, k // 2), "w_codes", dev), _arg(w_scales, u8, (E, n, k // block), "w_scales", dev),
+        _arg(w_scale, torch.float32, (E,), "w_scale", dev, allow_none=True),
+        _arg(y, _out_dtype(shape), (R, n), "y", dev), _workspace_arg(ws, dev), ws.numel(), _raw_stream(stream, dev))
     _check(st, "moe_grouped_gemm_microscaled")
 
 

@@ -14,9 +14,12 @@
 //
 // All three kernels are bound by memory: quantisation reads 2 (bf16) or 4 (fp32)
 // bytes an element and writes 1/2 + 1/16 (NVFP4) or 1/2 + 1/32 (MXFP4); the way
-// back is the reverse. A thread takes 32 bytes of the wide side, two 16-byte
-// accesses, so a warp covers 1 KB of it without gaps; a block's threads (1 to 4)
-// find amax with shuffles.
+// back is the reverse. A thread takes 32 bytes of the wide side in one access, so that
+// a warp covers 1 KB of it in whole sectors (two 16-byte accesses a thread instead:
+// dequantisation of 32768 x 2048 took 46 us, AFTER this way), and two such pieces at a
+// time; a block's threads (1 to 4) find amax with shuffles. Quantisation goes from the
+// end of a group to its start: what the tensor scale's pass has just read is still in
+// L2 there.
 #include "moe_internal.h"
 #include "sm100.cuh"
 
@@ -32,12 +35,36 @@ constexpr int elems_per_thread() {
   return 32 / static_cast<int>(sizeof(T));
 }
 
+// 32 bytes, one access.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Those of buffers that start at a multiple of 16 only.
+__device__ __forceinline__ void load16x2(const void* p, uint32_t (&w)[8]) {
+  const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+__device__ __forceinline__ void store16x2(void* p, const uint32_t (&w)[8]) {
+  static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // 32 bytes of input as fp32 values.
 template <typename T>
-__device__ __forceinline__ void load_row32(const T* src, float (&v)[elems_per_thread<T>()]) {
-  const uint4* s4 = reinterpret_cast<const uint4*>(src);
-  const uint4 a = __ldg(s4), b = __ldg(s4 + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void widen(const uint32_t (&w)[8], float (&v)[elems_per_thread<T>()]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (sizeof(T) == 4) {
@@ -118,15 +145,71 @@ __device__ __noinline__ uint32_t nv_settle(const float (&v)[8], uint32_t lo, uin
   return out;
 }
 
-// NV: NVFP4, else MXFP4. One 32-byte piece of the input per thread and turn.
+// The codes (EPT / 8 words) and the scale byte of one piece of a block; all lanes of the
+// warp together.
+template <typename T, bool NV>
+__device__ __forceinline__ void quantize_piece(const float (&v)[elems_per_thread<T>()], float g, float inv6g, bool g_ok,
+                                               uint32_t (&word)[elems_per_thread<T>() / 8], uint32_t& sbyte) {
+  constexpr int EPT = elems_per_thread<T>();
+  constexpr int TPB = (NV ? 16 : 32) / EPT;  // threads that share a block
+  // magnitudes compare as integers; an infinity or a NaN is above every number
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < TPB; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool bad = top >= 0x7F800000u || !g_ok;
+  float s, inv;
+  if constexpr (NV) {
+    sbyte = bad ? 0x7Fu : nv_scale(__uint_as_float(top), g, inv6g);
+    s = e4m3_value(sbyte);
+    inv = sbyte == 0 ? 0.0f : 1.0f / (s * g);
+  } else {
+    const uint32_t e = top >> 23;
+    sbyte = bad ? 0xFFu : (e < 2u ? 0u : e - 2u);
+    s = 0.0f;
+    inv = __uint_as_float((254u - (bad ? 127u : sbyte)) << 23);  // 2^(127 - sbyte): the products below are exact
+  }
+#pragma unroll
+  for (int h = 0; h < EPT / 8; ++h) {
+    float q[8], t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[8 * h + i] * inv;
+    if constexpr (NV) {
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        t[i] = q[i] * kBelow;
+        u[i] = q[i] * kAbove;
+      }
+      const uint32_t lo = cvt_e2m1x8(t), hi = cvt_e2m1x8(u);
+      word[h] = lo;
+      if (lo != hi) {
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i];
+        word[h] = nv_settle(w, lo, hi, s, g);
+      }
+    } else {
+      word[h] = cvt_e2m1x8(q);
+    }
+    if (bad) word[h] = 0u;
+  }
+}
+
+constexpr int kPieces = 2;  // pieces of a thread a turn, kThreads apart
+
+// NV: NVFP4, else MXFP4.
 template <typename T, bool NV>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T* __restrict__ x, const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales, int64_t groups, int64_t pieces_per_group) {
   constexpr int EPT = elems_per_thread<T>();
-  constexpr int TPB = (NV ? 16 : 32) / EPT;  // threads that share a block
+  constexpr int TPB = (NV ? 16 : 32) / EPT;
   pdl_trigger();
   pdl_wait();
+  const bool wide = aligned32(x);
+  const int64_t turns = (pieces_per_group + kPieces * kThreads - 1) / (kPieces * kThreads);
   for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
     float g = 1.0f, inv6g = 0.0f;
     bool g_ok = true;
@@ -136,70 +219,37 @@ __global__ void __launch_bounds__(kThreads)
       inv6g = 1.0f / (6.0f * g);
     }
     const int64_t first = grp * pieces_per_group;
-    // whole warps stay in the loop together (the shuffles below are warp-wide)
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads; base < pieces_per_group;
-         base += static_cast<int64_t>(gridDim.x) * kThreads) {
-      const int64_t p = base + threadIdx.x;
-      const bool live = p < pieces_per_group;
-      float v[EPT];
-      if (live) {
-        load_row32(x + (first + p) * EPT, v);
-      } else {
+    // whole warps stay in the loop together (quantize_piece's shuffles are warp-wide)
+    for (int64_t turn = turns - 1 - blockIdx.x; turn >= 0; turn -= gridDim.x) {
+      const int64_t p0 = turn * (kPieces * kThreads) + threadIdx.x;
+      uint32_t raw[kPieces][8];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
-      }
-      // magnitudes compare as integers; an infinity or a NaN is above every number
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int o = 1; o < TPB; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool bad = top >= 0x7F800000u || !g_ok;
-      uint32_t sbyte;
-      float s, inv;
-      if constexpr (NV) {
-        sbyte = bad ? 0x7Fu : nv_scale(__uint_as_float(top), g, inv6g);
-        s = e4m3_value(sbyte);
-        inv = sbyte == 0 ? 0.0f : 1.0f / (s * g);
-      } else {
-        const uint32_t e = top >> 23;
-        sbyte = bad ? 0xFFu : (e < 2u ? 0u : e - 2u);
-        s = 0.0f;
-        inv = __uint_as_float((254u - (bad ? 127u : sbyte)) << 23);  // 2^(127 - sbyte): the products below are exact
-      }
-      uint32_t word[EPT / 8];
-#pragma unroll
-      for (int h = 0; h < EPT / 8; ++h) {
-        float q[8], t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = v[8 * h + i] * inv;
-        if constexpr (NV) {
-          float u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            t[i] = q[i] * kBelow;
-            u[i] = q[i] * kAbove;
-          }
-          const uint32_t lo = cvt_e2m1x8(t), hi = cvt_e2m1x8(u);
-          word[h] = lo;
-          if (lo != hi) {
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i];
-            word[h] = nv_settle(w, lo, hi, s, g);
-          }
+      for (int j = 0; j < kPieces; ++j) {
+        const int64_t p = p0 + j * kThreads;
+        if (p < pieces_per_group) {
+          if (wide)
+            load32(x + (first + p) * EPT, raw[j]);
+          else
+            load16x2(x + (first + p) * EPT, raw[j]);
         } else {
-          word[h] = cvt_e2m1x8(q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) raw[j][i] = 0u;
         }
-        if (bad) word[h] = 0u;
       }
-      if (live) {
-        if constexpr (EPT == 16)
-          *reinterpret_cast<uint2*>(codes + (first + p) * 8) = make_uint2(word[0], word[EPT / 8 - 1]);
-        else
-          *reinterpret_cast<uint32_t*>(codes + (first + p) * 4) = word[0];
-        if (TPB == 1 || (threadIdx.x & (TPB - 1)) == 0)
-          scales[(first + p) / TPB] = static_cast<uint8_t>(sbyte);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int64_t p = p0 + j * kThreads;
+        float v[EPT];
+        widen<T>(raw[j], v);
+        uint32_t word[EPT / 8], sbyte;
+        quantize_piece<T, NV>(v, g, inv6g, g_ok, word, sbyte);
+        if (p < pieces_per_group) {
+          if constexpr (EPT == 16)
+            *reinterpret_cast<uint2*>(codes + (first + p) * 8) = make_uint2(word[0], word[EPT / 8 - 1]);
+          else
+            *reinterpret_cast<uint32_t*>(codes + (first + p) * 4) = word[0];
+          if (TPB == 1 || (threadIdx.x & (TPB - 1)) == 0) scales[(first + p) / TPB] = static_cast<uint8_t>(sbyte);
+        }
       }
     }
   }
@@ -224,51 +274,63 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int TPB = (NV ? 16 : 32) / EPT;
   pdl_trigger();
   pdl_wait();
+  const bool wide = aligned32(out);
   for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
     float g = 1.0f;
     if (NV && tensor_scale != nullptr) g = tensor_scale[grp];
     const int64_t first = grp * pieces_per_group;
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces_per_group;
-         p += static_cast<int64_t>(gridDim.x) * kThreads) {
-      const int64_t at = first + p;
-      uint32_t w[EPT / 8];
-      if constexpr (EPT == 16) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + at * 8));
-        w[0] = c.x;
-        w[EPT / 8 - 1] = c.y;
-      } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(codes + at * 4));
-      }
-      const uint32_t b = __ldg(scales + at / TPB) & (NV ? 0x7Fu : 0xFFu);
-      float s;
-      if constexpr (NV)
-        s = b == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(b);
-      else
-        s = b == 255u ? __uint_as_float(0x7FC00000u) : (b == 0u ? 0x1p-127f : __uint_as_float(b << 23));
-      float v[EPT];
+    for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * (kPieces * kThreads) + threadIdx.x; p0 < pieces_per_group;
+         p0 += static_cast<int64_t>(gridDim.x) * (kPieces * kThreads)) {
+      uint32_t w[kPieces][EPT / 8], sbyte[kPieces];
 #pragma unroll
-      for (int h = 0; h < EPT / 8; ++h) {
-        float t[8];
-        e2m1x8_scaled(w[h], t);
-        // the first two products are exact (6 significant bits), so a value is rounded once
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = t[i] * 0x1p126f * s;
-          v[8 * h + i] = NV ? e * g : e;
+      for (int j = 0; j < kPieces; ++j) {
+        const int64_t at = first + p0 + j * kThreads;
+        if (p0 + j * kThreads < pieces_per_group) {
+          if constexpr (EPT == 16) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + at * 8));
+            w[j][0] = c.x;
+            w[j][EPT / 8 - 1] = c.y;
+          } else {
+            w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(codes + at * 4));
+          }
+          sbyte[j] = __ldg(scales + at / TPB) & (NV ? 0x7Fu : 0xFFu);
         }
       }
-      uint4 o[2];
-      uint32_t* ow = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (sizeof(T) == 4)
-          ow[i] = __float_as_uint(v[i]);
+      for (int j = 0; j < kPieces; ++j) {
+        if (p0 + j * kThreads >= pieces_per_group) break;
+        const uint32_t b = sbyte[j];
+        float s;
+        if constexpr (NV)
+          s = b == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(b);
         else
-          ow[i] = pack_bf16x2(v[(2 * i) % EPT], v[(2 * i + 1) % EPT]);
+          s = b == 255u ? __uint_as_float(0x7FC00000u) : (b == 0u ? 0x1p-127f : __uint_as_float(b << 23));
+        float v[EPT];
+#pragma unroll
+        for (int h = 0; h < EPT / 8; ++h) {
+          float t[8];
+          e2m1x8_scaled(w[j][h], t);
+          // the first two products are exact (6 significant bits), so a value is rounded once
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float e = t[i] * 0x1p126f * s;
+            v[8 * h + i] = NV ? e * g : e;
+          }
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (sizeof(T) == 4)
+            o[i] = __float_as_uint(v[i]);
+          else
+            o[i] = pack_bf16x2(v[(2 * i) % EPT], v[(2 * i + 1) % EPT]);
+        }
+        T* dst = out + (first + p0 + j * kThreads) * EPT;
+        if (wide)
+          store32(dst, o);
+        else
+          store16x2(dst, o);
       }
-      uint4* dst = reinterpret_cast<uint4*>(out + at * EPT);
-      dst[0] = o[0];
-      dst[1] = o[1];
     }
   }
 }
@@ -276,54 +338,117 @@ __global__ void __launch_bounds__(kThreads)
 // scale[group] = max(amax / 2688, 2^-100) over the finite elements: 2688 = 6 * 448
 // puts the largest block scale at E4M3's largest number. Division and the lower
 // bound keep the order of their arguments, so each CTA divides its own amax and the
-// largest result is the group's; non-negative fp32 numbers order as integers. With
-// one CTA a group it is stored, else combined by an integer atomic maximum (whose
-// order does not matter) over a zeroed array.
-template <typename T>
+// largest result is the group's; non-negative fp32 numbers order as integers. The CTAs
+// of a group are a cluster, whose first gathers the others' results in its shared
+// memory; a few large groups have more CTAs each than a cluster holds and combine by an
+// integer atomic maximum (whose order does not matter) over a zeroed array.
+constexpr int kMaxCluster = 8;
+
+template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads)
     tensor_scale_kernel(const T* __restrict__ x, float* __restrict__ scale, int64_t groups, int64_t pieces_per_group) {
   constexpr int EPT = elems_per_thread<T>();
+  constexpr int U = 4;
   __shared__ uint32_t warp_top[kThreads / 32];
+  __shared__ uint32_t cta_top[kMaxCluster];
   pdl_trigger();
   pdl_wait();
+  const bool wide = aligned32(x);
   for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
     const T* src = x + grp * pieces_per_group * EPT;
     uint32_t top = 0;
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces_per_group;
-         p += static_cast<int64_t>(gridDim.x) * kThreads) {
-      float v[EPT];
-      load_row32(src + p * EPT, v);
+    for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * (U * kThreads) + threadIdx.x; p0 < pieces_per_group;
+         p0 += static_cast<int64_t>(gridDim.x) * (U * kThreads)) {
+      uint32_t raw[U][8];
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        top = max(top, m < 0x7F800000u ? m : 0u);
+      for (int j = 0; j < U; ++j) {
+        const int64_t p = p0 + j * kThreads;
+        if (p < pieces_per_group) {
+          if (wide)
+            load32(src + p * EPT, raw[j]);
+          else
+            load16x2(src + p * EPT, raw[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) raw[j][i] = 0u;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float v[EPT];
+        widen<T>(raw[j], v);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+          top = max(top, m < 0x7F800000u ? m : 0u);
+        }
       }
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
     __syncthreads();
+    uint32_t mine = 0;
     if (threadIdx.x == 0) {
 #pragma unroll
       for (int i = 1; i < kThreads / 32; ++i) top = max(top, warp_top[i]);
-      const float s = fmaxf(__uint_as_float(top) / 2688.0f, kMinTensorScale);
+      mine = __float_as_uint(fmaxf(__uint_as_float(top) / 2688.0f, kMinTensorScale));
+    }
+    if constexpr (CLUSTER) {
+      if (threadIdx.x == 0) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&cta_top[blockIdx.x]), 0)), "r"(mine)
+                     : "memory");
+      }
+      __syncwarp();
+      cluster_sync_all();
+      if (blockIdx.x == 0 && threadIdx.x == 0) {
+        for (unsigned i = 1; i < gridDim.x; ++i) mine = max(mine, cta_top[i]);
+        scale[grp] = __uint_as_float(mine);
+      }
+      __syncwarp();
+      cluster_sync_all();  // read before the next group's results come
+    } else if (threadIdx.x == 0) {
       if (gridDim.x == 1)
-        scale[grp] = s;
+        scale[grp] = __uint_as_float(mine);
       else
-        atomicMax(reinterpret_cast<unsigned int*>(scale + grp), __float_as_uint(s));
+        atomicMax(reinterpret_cast<unsigned int*>(scale + grp), mine);
     }
     __syncthreads();
   }
 }
 
 // CTAs: enough to fill the device (8 of 256 threads an SM), no more than there is
-// work for; a group each in y.
-dim3 piece_grid(int64_t groups, int64_t pieces_per_group, int per_sm) {
-  const int64_t want = static_cast<int64_t>(device_sm_count()) * per_sm;
+// work for (per_turn pieces a CTA); a group each in y.
+dim3 piece_grid(int64_t groups, int64_t pieces_per_group, int64_t per_turn) {
+  const int64_t want = static_cast<int64_t>(device_sm_count()) * 8;
   const int64_t gy = groups < 65535 ? groups : 65535;
-  int64_t gx = (pieces_per_group + kThreads - 1) / kThreads;
+  int64_t gx = (pieces_per_group + per_turn - 1) / per_turn;
   const int64_t share = (want + gy - 1) / gy;
   if (gx > share) gx = share;
   return dim3(static_cast<unsigned>(gx < 1 ? 1 : gx), static_cast<unsigned>(gy));
+}
+
+template <typename T>
+cudaError_t run_tensor_scale(int64_t groups, int64_t pieces, const void* x, float* scale, cudaStream_t st) {
+  dim3 grid = piece_grid(groups, pieces, 4 * kThreads);
+  const T* typed = static_cast<const T*>(x);
+  // A cluster a group saves the launch that zeroes `scale` (about 2 us): where a group
+  // has no work for more CTAs, or up to eight turns a CTA (64 KB each) more than with them.
+  if (grid.x > 1 && (grid.x <= kMaxCluster || pieces <= 8 * 4 * kThreads * kMaxCluster)) {
+    if (grid.x > kMaxCluster) grid.x = kMaxCluster;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    return launch_dependent(tensor_scale_kernel<T, true>, grid, dim3(kThreads), 0, st, attr, 1, typed, scale, groups,
+                            pieces);
+  }
+  if (grid.x > 1) {
+    const cudaError_t e = cudaMemsetAsync(scale, 0, static_cast<size_t>(groups) * 4, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(tensor_scale_kernel<T, false>, grid, dim3(kThreads), 0, st, nullptr, 0, typed, scale, groups,
+                          pieces);
 }
 
 }  // namespace
@@ -331,22 +456,14 @@ dim3 piece_grid(int64_t groups, int64_t pieces_per_group, int per_sm) {
 cudaError_t launch_tensor_scale(int64_t groups, int64_t per_group, bool fp32, const void* x, float* scale,
                                 cudaStream_t st) {
   const int64_t pieces = per_group / (fp32 ? 8 : 16);
-  const dim3 grid = piece_grid(groups, pieces, 8);
-  if (grid.x > 1) {
-    const cudaError_t e = cudaMemsetAsync(scale, 0, static_cast<size_t>(groups) * 4, st);
-    if (e != cudaSuccess) return e;
-  }
-  if (fp32)
-    return launch_dependent(tensor_scale_kernel<float>, grid, dim3(kThreads), 0, st, nullptr, 0,
-                            static_cast<const float*>(x), scale, groups, pieces);
-  return launch_dependent(tensor_scale_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, nullptr, 0,
-                          static_cast<const __nv_bfloat16*>(x), scale, groups, pieces);
+  return fp32 ? run_tensor_scale<float>(groups, pieces, x, scale, st)
+              : run_tensor_scale<__nv_bfloat16>(groups, pieces, x, scale, st);
 }
 
 cudaError_t launch_quantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const void* x,
                             const float* tensor_scale, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   const int64_t pieces = per_group / (fp32 ? 8 : 16);
-  const dim3 grid = piece_grid(groups, pieces, 8);
+  const dim3 grid = piece_grid(groups, pieces, kPieces * kThreads);
   auto go = [&](auto kern, auto* typed) {
     return launch_dependent(kern, grid, dim3(kThreads), 0, st, nullptr, 0, typed, tensor_scale, codes, scales, groups,
                             pieces);
@@ -360,7 +477,7 @@ cudaError_t launch_quantize(bool nv, int64_t groups, int64_t per_group, bool fp3
 cudaError_t launch_dequantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const uint8_t* codes,
                               const uint8_t* scales, const float* tensor_scale, void* out, cudaStream_t st) {
   const int64_t pieces = per_group / (fp32 ? 8 : 16);
-  const dim3 grid = piece_grid(groups, pieces, 8);
+  const dim3 grid = piece_grid(groups, pieces, kPieces * kThreads);
   auto go = [&](auto kern, auto* typed) {
     return launch_dependent(kern, grid, dim3(kThreads), 0, st, nullptr, 0, codes, scales, tensor_scale, typed, groups,
                             pieces);
