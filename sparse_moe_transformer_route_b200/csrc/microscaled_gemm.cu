@@ -67,20 +67,24 @@ struct QCfg {
   static constexpr uint32_t SFB_COL = SFA_COL + WORDS * 4;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int EPI_WARPS = 8;
+  // scale warps: one for each 128 rows, in sets that take the slots in turn, so that the
+  // loads of some are in flight while others write
   static constexpr int SF_WARPS = 1 + BBLK;
-  static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS + 1);
+  static constexpr int SF_SETS = 4;
+  static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_SETS * SF_WARPS + 1);
   static constexpr int CHUNKS = (BN + 63) / 64;  // 32-column chunks of an epilogue warp
   static constexpr int MISC_BYTES = 1024 + static_cast<int>(sizeof(RaggedGroups));
   static constexpr int ROOM = 227 * 1024 - 1024 - MISC_BYTES;
-  static constexpr int STAGES_FIT = (ROOM - (PAIR ? 5 : 2) * SF_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES_FIT = (ROOM - 4 * SF_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   // the scales' way is longer by a pass through registers: their ring reaches further
   static constexpr int SF_FIT = (ROOM - STAGES * STAGE_BYTES) / SF_BYTES;
-  static constexpr int SF_SLOTS = SF_FIT > 8 ? 8 : SF_FIT;
+  // (a multiple of the sets: a slot is always the same set's, which has then seen every
+  // phase of its barriers)
+  static constexpr int SF_SLOTS = (SF_FIT > 8 ? 8 : SF_FIT) / SF_SETS * SF_SETS;
   static constexpr size_t SMEM_BYTES =
       1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + static_cast<size_t>(SF_SLOTS) * SF_BYTES + MISC_BYTES;
-  static constexpr int AHEAD = 2;  // slots whose scales one batch of loads brings to registers
-  static_assert(STAGES >= 3 && SF_SLOTS >= 2 && (2 * STAGES + 3 * SF_SLOTS + 6) * 8 <= 1024, "rings");
+  static_assert(STAGES >= 3 && SF_SLOTS >= 4 && SF_SLOTS % SF_SETS == 0 && (2 * STAGES + 3 * SF_SLOTS + 6) * 8 <= 1024, "rings");
   static_assert(SMEM_BYTES > 114 * 1024, "one CTA an SM");
   static_assert(SFB_COL + WORDS * 4 * BBLK <= 512, "TMEM columns");
   static_assert(BN == 256 || (!PAIR && (BN == 128 || BN == 64 || BN == 32)), "tile N");
@@ -175,33 +179,49 @@ __device__ __forceinline__ QTile q_tile(const QArgs& a, const RaggedGroups& g, i
   return t;
 }
 
-// N words of a scale row from byte `at` on, zero past the row's end. The row starts at
-// any address: the words that cover the piece are read at multiples of four and shifted
-// together, but for what would lie past `end`, the buffer's end, which is read byte by
-// byte.
-template <int N>
-__device__ __forceinline__ void load_scale_words(uint32_t (&w)[N], const uint8_t* row, int at, int row_bytes,
+// Eight words of a scale row from byte `at` on, zero past the row's end. The row starts
+// at any address: the (up to three) 16-byte pieces that cover the words are read whole
+// and shifted together, but for one that would leave the buffer at `end`, which is read
+// byte by byte.
+__device__ __forceinline__ void load_scale_words(uint32_t (&w)[8], const uint8_t* row, int at, int row_bytes,
                                                  const uint8_t* end) {
   const uint8_t* p = row + at;
-  const int bytes = min(4 * N, row_bytes - at);
-  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+  const int bytes = min(32, row_bytes - at);
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
   const uint8_t* base = p - off;
-  uint32_t v[N + 1];
+  uint32_t v[12];
 #pragma unroll
-  for (int i = 0; i <= N; ++i) {
-    v[i] = 0u;
-    if (4 * i < bytes + static_cast<int>(off)) {
-      if (base + 4 * i + 4 <= end) {
-        v[i] = __ldg(reinterpret_cast<const uint32_t*>(base) + i);
+  for (int i = 0; i < 3; ++i) {
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (16 * i < bytes + static_cast<int>(off)) {
+      if (base + 16 * i + 16 <= end) {
+        q = __ldg(reinterpret_cast<const uint4*>(base) + i);
       } else {
-        for (int b = 0; b < 4; ++b)
-          if (base + 4 * i + b < end) v[i] |= static_cast<uint32_t>(__ldg(base + 4 * i + b)) << (8 * b);
+        for (int b = 0; base + 16 * i + b < end; ++b) {
+          const uint32_t byte = static_cast<uint32_t>(__ldg(base + 16 * i + b)) << (8 * (b & 3));
+          if (b < 4) q.x |= byte;
+          else if (b < 8) q.y |= byte;
+          else if (b < 12) q.z |= byte;
+          else q.w |= byte;
+        }
       }
     }
+    v[4 * i] = q.x;
+    v[4 * i + 1] = q.y;
+    v[4 * i + 2] = q.z;
+    v[4 * i + 3] = q.w;
+  }
+  if (off & 8u) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) v[i] = v[i + 2];
+  }
+  if (off & 4u) {
+#pragma unroll
+    for (int i = 0; i < 9; ++i) v[i] = v[i + 1];
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+  for (int i = 0; i < 8; ++i) {
+    w[i] = __funnelshift_r(v[i], v[i + 1], 8 * (off & 3u));
     const int have = bytes - 4 * i;  // bytes of this word that belong to the row
     if (have < 4) w[i] &= have <= 0 ? 0u : (1u << (8 * have)) - 1u;
   }
@@ -494,16 +514,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
   } else {
-    // ------------------------------------------------ scale warps: warp 0 of these the
-    // rows of A, then a 128-row block of B each, the last the TMA producer
-    const int who = warp - 2 - C::EPI_WARPS;
+    // ------------------------------------------------ scale warps: warp 0 of a set the
+    // rows of A, then a 128-row block of B each; after the sets the TMA producer
+    const int sf_warp = warp - 2 - C::EPI_WARPS;
+    const bool producer = sf_warp == C::SF_SETS * C::SF_WARPS;
+    const int set = sf_warp / C::SF_WARPS, who = sf_warp % C::SF_WARPS;
     const int my_tiles = first_tile < n_tiles ? (n_tiles - 1 - first_tile) / grid + 1 : 0;
     unsigned char* const block0 = sf_base + who * C::SF_BLOCK;
-    int slot = 0;
+    const int stride = producer ? 1 : C::SF_SETS;
+    int slot = producer ? 0 : set;
     uint32_t phase = 0;
     auto step = [&]() {
-      if (++slot == C::SF_SLOTS) {
-        slot = 0;
+      slot += stride;
+      if (slot >= C::SF_SLOTS) {
+        slot -= C::SF_SLOTS;
         phase ^= 1u;
       }
     };
@@ -524,7 +548,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       step();
     };
     const int slots = (nk + C::SF_STAGES_PER - 1) / C::SF_STAGES_PER;  // of a tile
-    if (who == C::SF_WARPS) {
+    if (producer) {
       if (a.tma_scales) {
         int issued = 0;
         bool ok = true;
@@ -563,7 +587,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     } else if (a.tma_scales) {
-      for (int i = 0; i < my_tiles * slots; ++i) {
+      for (int i = set; i < my_tiles * slots; i += C::SF_SETS) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[slot], phase))) {
           if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
           break;
@@ -587,10 +611,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         hand_over(r);
       }
     } else {
-      // through registers, AHEAD slots at a time
+      // through registers
       const int row_bytes = a.k / (C::NV ? 16 : 32);
       const uint8_t* end = who == 0 ? a.ws + static_cast<int64_t>(a.E) * a.n * row_bytes : a.xs + a.rows * row_bytes;
-      int lL = first_tile, lj = 0;
+      int lL = first_tile, lj = set;
       const uint8_t* src[4];
       bool live[4];
       auto aim = [&]() {
@@ -610,43 +634,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       };
-      aim();
-      uint32_t buf[C::AHEAD][4][8];
-      auto fetch = [&](uint32_t (&b)[4][8]) {
-        if (lL >= n_tiles) return;
+      bool aimed = false;
+      for (int i = set; i < my_tiles * slots; i += C::SF_SETS) {
+        while (lj >= slots) {
+          lj -= slots;
+          lL += grid;
+          aimed = false;
+        }
+        if (!aimed) aim();
+        aimed = true;
+        uint32_t r[4][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (live[i]) {
-            load_scale_words<8>(b[i], src[i], lj * 32, row_bytes, end);
+        for (int q = 0; q < 4; ++q) {
+          if (live[q]) {
+            load_scale_words(r[q], src[q], lj * 32, row_bytes, end);
           } else {
 #pragma unroll
-            for (int w = 0; w < 8; ++w) b[i][w] = 0u;
+            for (int w = 0; w < 8; ++w) r[q][w] = 0u;
           }
         }
-        if (++lj == slots) {
-          lj = 0;
-          lL += grid;
-          aim();
+        lj += C::SF_SETS;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase ^ 1u))) {
+          if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
+          break;
         }
-      };
-      const int total = my_tiles * slots;
-      bool ok = true;
-      for (int it = 0; it < total && ok; it += C::AHEAD) {
-        // all loads of a batch, then their stores: the fence in hand_over waits for
-        // whatever the warp has in flight
-#pragma unroll
-        for (int s = 0; s < C::AHEAD; ++s) fetch(buf[s]);
-#pragma unroll
-        for (int s = 0; s < C::AHEAD; ++s) {
-          if (it + s < total && ok) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase ^ 1u))) {
-              if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_PRODUCER);
-              ok = false;
-            } else {
-              hand_over(buf[s]);
-            }
-          }
-        }
+        hand_over(r);
       }
     }
   }
