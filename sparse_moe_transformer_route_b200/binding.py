@@ -534,6 +534,8 @@ def _current_device():
 
 def _raw_stream(stream, device):
     if stream is not None:
+        if stream.device_index != device:
+            raise ValueError(f"stream must be one of the current device (cuda:{device})")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device)  # current_stream() builds an object: 2 us
 

@@ -230,6 +230,31 @@ def test_no_rows_and_two_dimensions():
     same(c, want_c[0])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+def test_buffers_that_start_at_a_multiple_of_16_only(fmt, dtype):
+    """The wide side of a conversion is accessed 32 bytes at a time where it is aligned so."""
+    R, K = 37, 96
+    skip = 128 // torch.finfo(dtype).bits  # elements of 16 bytes
+    held = torch.randn(skip + R * K, device="cuda").to(dtype)
+    x = held[skip:].view(1, R, K)
+    assert x.data_ptr() % 32 == 16
+    g = None
+    if fmt == NV:
+        g = torch.empty(1, device="cuda")
+        M.moe_tensor_scale_microscaled(x, g)
+        assert g.item() == max((x.float().abs().max().double() / torch.tensor(2688.0).double()).float().item(), 2.0 ** -100)
+    codes, scales = quantize(x, g, fmt)
+    want_c, want_s = ref_quantize(x, g, fmt)
+    assert torch.equal(scales.cpu(), want_s)
+    same(codes, want_c)
+    held2 = torch.full((skip + R * K + skip,), 5.0, device="cuda").to(dtype)
+    out = held2[skip:-skip].view(1, R, K)
+    M.moe_dequantize_microscaled(fmt, codes, scales, g, out)
+    assert torch.equal(out.cpu(), ref_dequantize(unpack(codes), scales.cpu(), g, fmt, dtype))
+    assert torch.all(held2[:skip] == 5.0) and torch.all(held2[-skip:] == 5.0)
+
+
 def test_tensor_scale_of_many_sizes():
     """One CTA a group and many; results do not depend on the run."""
     for shape in ((1, 1, 32), (1, 5000, 2048), (300, 2, 32), (70000, 1, 32), (3, 999, 1056)):
@@ -306,6 +331,53 @@ def test_product_matches_64_bits(fmt, how, n, k):
                                         ([1], 2048, 2048), ([900, 900], 1416, 1056)])
 def test_product_matches_64_bits_larger(fmt, dt, counts, n, k):
     run_product(counts, n, k, fmt, dt, "gaps", seed=k)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("n,k,how", [(4096, 2048, "packed"), (4104, 2080, "gaps")])
+def test_product_of_large_groups_runs_on_pairs(fmt, n, k, how):
+    run_product([700, 1, 650, 0, 1303, 704, 257, 2000], n, k, fmt, BF, how, seed=k)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("mean,n,k", [(3, 512, 512), (30, 2048, 288), (80, 2048, 1024), (300, 128, 288), (300, 128, 512)])
+def test_product_every_kind_of_tile(fmt, mean, n, k):
+    g = torch.Generator().manual_seed(mean)
+    counts = torch.poisson(torch.full((64,), float(mean)), generator=g).int().tolist()
+    run_product(counts, n, k, fmt, BF, "packed", seed=mean)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+def test_product_of_most_experts(fmt):
+    g = torch.Generator().manual_seed(6)
+    run_product(torch.randint(0, 30, (256,), generator=g).tolist(), 72, 96, fmt, F32)
+
+
+@pytest.mark.parametrize("k", [4096, 4128])
+def test_product_far_rows(k):
+    """Codes beyond 2^31 bytes, scales by TMA (4096) and through registers (4128)."""
+    n, total = 16, (1 << 20) + 100
+    xc = torch.zeros(total, k // 2, dtype=U8, device="cuda")
+    xs = torch.zeros(total, k // 32, dtype=U8, device="cuda")
+    spans = ((total - 70, 65), (3, 5))
+    gs = torch.tensor([total - 70, 3, 0], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 65, 70], dtype=torch.int32, device="cuda")
+    x = torch.randn(1, 70, k, device="cuda")
+    c, s = quantize(x, None, MX)
+    for at, lo, hi in ((total - 70, 0, 65), (3, 65, 70)):
+        xc[at:at + hi - lo], xs[at:at + hi - lo] = c[0, lo:hi], s[0, lo:hi]
+    wc, wsc = quantize(torch.randn(2, n, k, device="cuda"), None, MX)
+    sh = M.grouped_shape(total, 2, n, k, F32)
+    ws = M.grouped_workspace(sh)
+    y = torch.zeros(total, n, device="cuda")
+    M.moe_grouped_gemm_microscaled(sh, MX, xc, xs, None, gs, off, wc, wsc, None, y, ws)
+    assert M.moe_get_device_status(ws) == 0
+    for e, (at, m) in enumerate(spans):
+        xe, we = values(xc[at:at + m], xs[at:at + m], None, MX), values(wc[e], wsc[e], None, MX)
+        ref, S = xe @ we.t(), xe.abs() @ we.abs().t()
+        tol = 2.0 ** -24 * ref.abs() + 65 * (k / 64 + 1) * 2.0 ** -23 * S
+        assert ((y[at:at + m].double() - ref).abs() <= tol).all()
+    assert torch.all(y[8:total - 70] == 0) and torch.all(y[total - 5:] == 0)
 
 
 @pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])

@@ -124,6 +124,23 @@ def test_products_match_64_bits_larger(counts, n, k, dt):
     run_all(counts, n, k, "gaps", dt, seed=k)
 
 
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("how", ["packed", "gaps"])
+@pytest.mark.parametrize("n,k", [(2048, 2048), (2056, 1032)])
+def test_large_groups_run_on_pairs(n, k, how, dt):
+    """Enough rows and columns for 256 x 256 tiles: groups that end anywhere in a tile, in a
+    64-row stage of wgrad's reduction and in a 16-row step, among them small and empty ones."""
+    run_all([700, 1, 650, 0, 1303, 704, 257, 2000], n, k, how, dt, seed=n)
+
+
+@pytest.mark.parametrize("mean,n", [(3, 512), (30, 2048), (80, 2048), (300, 128), (140, 384)])
+def test_every_kind_of_tile(mean, n):
+    """Mean group sizes and widths on both sides of the rule that picks a tile."""
+    g = torch.Generator().manual_seed(mean)
+    counts = torch.poisson(torch.full((64,), float(mean)), generator=g).int().tolist()
+    run_all(counts, n, 136, "packed", BF, seed=mean)
+
+
 def test_most_experts_with_random_counts():
     g = torch.Generator().manual_seed(5)
     counts = torch.randint(0, 40, (256,), generator=g).tolist()
@@ -302,6 +319,61 @@ def test_captured_graph_follows_its_inputs():
             check(y[s:s + c], xe @ we.t(), xe.abs() @ we.abs().t(), k, f"y of expert {e}")
             check(dx[s:s + c], de @ we, de.abs() @ we.abs(), n, f"dx of expert {e}")
             check(dw[e], de.t() @ xe, de.abs().t() @ xe.abs(), c, f"dW of expert {e}")
+
+
+def test_two_graphs_share_a_workspace_and_operands():
+    """Two captured calls, replayed on two streams at once."""
+    gs, off, starts, total, x, dy, w, _ = make([300, 77, 0, 900], 512, 256, "packed", seed=8)
+    sh, shx = M.grouped_shape(total, 4, 512, 256, F32), M.grouped_shape(total, 4, 512, 256, BF)
+    ws = M.grouped_workspace(sh)
+    dw, dx = torch.zeros(4, 512, 256, device="cuda"), torch.zeros(total, 256, dtype=BF, device="cuda")
+    graphs = []
+    for call in (lambda: M.moe_grouped_gemm_wgrad(sh, dy, x, gs, off, dw, ws),
+                 lambda: M.moe_grouped_gemm_dgrad(shx, dy, gs, off, w, dx, ws)):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, torch.cuda.Stream()))
+    want = dw.clone(), dx.clone()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert M.moe_get_device_status(ws) == 0
+    assert torch.equal(dw, want[0]) and torch.equal(dx, want[1])
+    for e, (s, c) in enumerate(zip(starts, [300, 77, 0, 900])):
+        xe, de, we = x[s:s + c].double(), dy[s:s + c].double(), w[e].double()
+        check(dx[s:s + c], de @ we, de.abs() @ we.abs(), 512, f"dx of expert {e}")
+        check(dw[e], de.t() @ xe, de.abs().t() @ xe.abs(), c, f"dW of expert {e}")
+
+
+def test_calls_want_the_current_stream_and_device():
+    x = torch.zeros(4, 64, dtype=BF, device="cuda")
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    w, y = torch.zeros(1, 64, 64, dtype=BF, device="cuda"), torch.zeros(4, 64, dtype=BF, device="cuda")
+    sh = M.grouped_shape(4, 1, 64, 64)
+    ws = M.grouped_workspace(sh)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        M.moe_grouped_gemm(sh, x.cpu(), None, off, w, y, ws)
+    with pytest.raises(ValueError, match="w must be contiguous"):
+        M.moe_grouped_gemm(sh, x, None, off, w.transpose(1, 2), y, ws)
+    with pytest.raises(TypeError, match="y must be torch.bfloat16"):
+        M.moe_grouped_gemm(sh, x, None, off, w, y.float(), ws)
+    with pytest.raises(M.MoeError) as err:
+        M.moe_grouped_gemm(sh, x, None, off, w, y, ws[:128])
+    assert err.value.status == 3
+    if torch.cuda.device_count() > 1:
+        with pytest.raises(ValueError, match="current device"):
+            M.moe_grouped_gemm(sh, x.to("cuda:1"), None, off, w, y, ws)
+        with pytest.raises(ValueError, match="stream"):
+            M.moe_grouped_gemm(sh, x, None, off, w, y, ws, stream=torch.cuda.Stream("cuda:1"))
 
 
 def test_far_rows_of_a_large_buffer():
