@@ -16,10 +16,12 @@
 // bytes an element and writes 1/2 + 1/16 (NVFP4) or 1/2 + 1/32 (MXFP4); the way
 // back is the reverse. A thread takes 32 bytes of the wide side in one access, so that
 // a warp covers 1 KB of it in whole sectors (two 16-byte accesses a thread instead:
-// dequantisation of 32768 x 2048 took 46 us, AFTER this way), and two such pieces at a
-// time; a block's threads (1 to 4) find amax with shuffles. Quantisation goes from the
-// end of a group to its start: what the tensor scale's pass has just read is still in
-// L2 there.
+// dequantisation of 32768 x 2048 took 46 us, 29 this way), and four such pieces, all
+// loads before the first use, in CTAs that end with them: 64 weights of 2048 x 2048 to
+// bf16 take 107 us, 117 with CTAs that stay and loop, 135 with one piece at a time. Small
+// tensors take one piece a thread, which reaches four times as many SMs. A block's
+// threads (1 to 4) find amax with shuffles. Quantisation goes from the end of a group to
+// its start: what the tensor scale's pass has just read is still in L2 there.
 #include "moe_internal.h"
 #include "sm100.cuh"
 
@@ -197,10 +199,8 @@ __device__ __forceinline__ void quantize_piece(const float (&v)[elems_per_thread
   }
 }
 
-constexpr int kPieces = 2;  // pieces of a thread a turn, kThreads apart
-
-// NV: NVFP4, else MXFP4.
-template <typename T, bool NV>
+// NV: NVFP4, else MXFP4. kPieces: pieces of a thread, kThreads apart.
+template <typename T, bool NV, int kPieces>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T* __restrict__ x, const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales, int64_t groups, int64_t pieces_per_group) {
@@ -209,7 +209,6 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
   pdl_wait();
   const bool wide = aligned32(x);
-  const int64_t turns = (pieces_per_group + kPieces * kThreads - 1) / (kPieces * kThreads);
   for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
     float g = 1.0f, inv6g = 0.0f;
     bool g_ok = true;
@@ -219,37 +218,35 @@ __global__ void __launch_bounds__(kThreads)
       inv6g = 1.0f / (6.0f * g);
     }
     const int64_t first = grp * pieces_per_group;
-    // whole warps stay in the loop together (quantize_piece's shuffles are warp-wide)
-    for (int64_t turn = turns - 1 - blockIdx.x; turn >= 0; turn -= gridDim.x) {
-      const int64_t p0 = turn * (kPieces * kThreads) + threadIdx.x;
-      uint32_t raw[kPieces][8];
+    // (whole warps come here together: quantize_piece's shuffles are warp-wide)
+    const int64_t p0 = static_cast<int64_t>(gridDim.x - 1 - blockIdx.x) * (kPieces * kThreads) + threadIdx.x;
+    uint32_t raw[kPieces][8];
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const int64_t p = p0 + j * kThreads;
-        if (p < pieces_per_group) {
-          if (wide)
-            load32(x + (first + p) * EPT, raw[j]);
-          else
-            load16x2(x + (first + p) * EPT, raw[j]);
-        } else {
+    for (int j = 0; j < kPieces; ++j) {
+      const int64_t p = p0 + j * kThreads;
+      if (p < pieces_per_group) {
+        if (wide)
+          load32(x + (first + p) * EPT, raw[j]);
+        else
+          load16x2(x + (first + p) * EPT, raw[j]);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) raw[j][i] = 0u;
-        }
+        for (int i = 0; i < 8; ++i) raw[j][i] = 0u;
       }
+    }
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const int64_t p = p0 + j * kThreads;
-        float v[EPT];
-        widen<T>(raw[j], v);
-        uint32_t word[EPT / 8], sbyte;
-        quantize_piece<T, NV>(v, g, inv6g, g_ok, word, sbyte);
-        if (p < pieces_per_group) {
-          if constexpr (EPT == 16)
-            *reinterpret_cast<uint2*>(codes + (first + p) * 8) = make_uint2(word[0], word[EPT / 8 - 1]);
-          else
-            *reinterpret_cast<uint32_t*>(codes + (first + p) * 4) = word[0];
-          if (TPB == 1 || (threadIdx.x & (TPB - 1)) == 0) scales[(first + p) / TPB] = static_cast<uint8_t>(sbyte);
-        }
+    for (int j = 0; j < kPieces; ++j) {
+      const int64_t p = p0 + j * kThreads;
+      float v[EPT];
+      widen<T>(raw[j], v);
+      uint32_t word[EPT / 8], sbyte;
+      quantize_piece<T, NV>(v, g, inv6g, g_ok, word, sbyte);
+      if (p < pieces_per_group) {
+        if constexpr (EPT == 16)
+          *reinterpret_cast<uint2*>(codes + (first + p) * 8) = make_uint2(word[0], word[EPT / 8 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(codes + (first + p) * 4) = word[0];
+        if (TPB == 1 || (threadIdx.x & (TPB - 1)) == 0) scales[(first + p) / TPB] = static_cast<uint8_t>(sbyte);
       }
     }
   }
@@ -265,7 +262,7 @@ __device__ __forceinline__ void e2m1x8_scaled(uint32_t w, float (&v)[8]) {
   }
 }
 
-template <typename T, bool NV>
+template <typename T, bool NV, int kPieces>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                       const float* __restrict__ tensor_scale, T* __restrict__ out, int64_t groups,
@@ -279,58 +276,56 @@ __global__ void __launch_bounds__(kThreads)
     float g = 1.0f;
     if (NV && tensor_scale != nullptr) g = tensor_scale[grp];
     const int64_t first = grp * pieces_per_group;
-    for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * (kPieces * kThreads) + threadIdx.x; p0 < pieces_per_group;
-         p0 += static_cast<int64_t>(gridDim.x) * (kPieces * kThreads)) {
-      uint32_t w[kPieces][EPT / 8], sbyte[kPieces];
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * (kPieces * kThreads) + threadIdx.x;
+    uint32_t w[kPieces][EPT / 8], sbyte[kPieces];
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const int64_t at = first + p0 + j * kThreads;
-        if (p0 + j * kThreads < pieces_per_group) {
-          if constexpr (EPT == 16) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + at * 8));
-            w[j][0] = c.x;
-            w[j][EPT / 8 - 1] = c.y;
-          } else {
-            w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(codes + at * 4));
-          }
-          sbyte[j] = __ldg(scales + at / TPB) & (NV ? 0x7Fu : 0xFFu);
+    for (int j = 0; j < kPieces; ++j) {
+      const int64_t at = first + p0 + j * kThreads;
+      if (p0 + j * kThreads < pieces_per_group) {
+        if constexpr (EPT == 16) {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + at * 8));
+          w[j][0] = c.x;
+          w[j][EPT / 8 - 1] = c.y;
+        } else {
+          w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(codes + at * 4));
         }
+        sbyte[j] = __ldg(scales + at / TPB) & (NV ? 0x7Fu : 0xFFu);
       }
+    }
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        if (p0 + j * kThreads >= pieces_per_group) break;
-        const uint32_t b = sbyte[j];
-        float s;
-        if constexpr (NV)
-          s = b == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(b);
-        else
-          s = b == 255u ? __uint_as_float(0x7FC00000u) : (b == 0u ? 0x1p-127f : __uint_as_float(b << 23));
-        float v[EPT];
+    for (int j = 0; j < kPieces; ++j) {
+      if (p0 + j * kThreads >= pieces_per_group) break;
+      const uint32_t b = sbyte[j];
+      float s;
+      if constexpr (NV)
+        s = b == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(b);
+      else
+        s = b == 255u ? __uint_as_float(0x7FC00000u) : (b == 0u ? 0x1p-127f : __uint_as_float(b << 23));
+      float v[EPT];
 #pragma unroll
-        for (int h = 0; h < EPT / 8; ++h) {
-          float t[8];
-          e2m1x8_scaled(w[j][h], t);
-          // the first two products are exact (6 significant bits), so a value is rounded once
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float e = t[i] * 0x1p126f * s;
-            v[8 * h + i] = NV ? e * g : e;
-          }
-        }
-        uint32_t o[8];
+      for (int h = 0; h < EPT / 8; ++h) {
+        float t[8];
+        e2m1x8_scaled(w[j][h], t);
+        // the first two products are exact (6 significant bits), so a value is rounded once
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if constexpr (sizeof(T) == 4)
-            o[i] = __float_as_uint(v[i]);
-          else
-            o[i] = pack_bf16x2(v[(2 * i) % EPT], v[(2 * i + 1) % EPT]);
+          const float e = t[i] * 0x1p126f * s;
+          v[8 * h + i] = NV ? e * g : e;
         }
-        T* dst = out + (first + p0 + j * kThreads) * EPT;
-        if (wide)
-          store32(dst, o);
-        else
-          store16x2(dst, o);
       }
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4)
+          o[i] = __float_as_uint(v[i]);
+        else
+          o[i] = pack_bf16x2(v[(2 * i) % EPT], v[(2 * i + 1) % EPT]);
+      }
+      T* dst = out + (first + p0 + j * kThreads) * EPT;
+      if (wide)
+        store32(dst, o);
+      else
+        store16x2(dst, o);
     }
   }
 }
@@ -416,24 +411,25 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// CTAs: enough to fill the device (8 of 256 threads an SM), no more than there is
-// work for (per_turn pieces a CTA); a group each in y.
+// A CTA for every per_turn pieces of a group, a group each in y.
 dim3 piece_grid(int64_t groups, int64_t pieces_per_group, int64_t per_turn) {
-  const int64_t want = static_cast<int64_t>(device_sm_count()) * 8;
   const int64_t gy = groups < 65535 ? groups : 65535;
-  int64_t gx = (pieces_per_group + per_turn - 1) / per_turn;
-  const int64_t share = (want + gy - 1) / gy;
-  if (gx > share) gx = share;
+  const int64_t gx = (pieces_per_group + per_turn - 1) / per_turn;
   return dim3(static_cast<unsigned>(gx < 1 ? 1 : gx), static_cast<unsigned>(gy));
+}
+
+// Pieces of a thread: four once that fills the device's threads.
+bool four_pieces(int64_t groups, int64_t pieces_per_group) {
+  return groups * pieces_per_group >= static_cast<int64_t>(device_sm_count()) * 8 * kThreads;
 }
 
 template <typename T>
 cudaError_t run_tensor_scale(int64_t groups, int64_t pieces, const void* x, float* scale, cudaStream_t st) {
   dim3 grid = piece_grid(groups, pieces, 4 * kThreads);
   const T* typed = static_cast<const T*>(x);
-  // A cluster a group saves the launch that zeroes `scale` (about 2 us): where a group
-  // has no work for more CTAs, or up to eight turns a CTA (64 KB each) more than with them.
-  if (grid.x > 1 && (grid.x <= kMaxCluster || pieces <= 8 * 4 * kThreads * kMaxCluster)) {
+  // A cluster a group saves the launch that zeroes `scale` (about 2 us): where its CTAs
+  // take at most eight turns (of 32 KB).
+  if (grid.x > 1 && pieces <= 8 * 4 * kThreads * kMaxCluster) {
     if (grid.x > kMaxCluster) grid.x = kMaxCluster;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -463,29 +459,41 @@ cudaError_t launch_tensor_scale(int64_t groups, int64_t per_group, bool fp32, co
 cudaError_t launch_quantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const void* x,
                             const float* tensor_scale, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   const int64_t pieces = per_group / (fp32 ? 8 : 16);
-  const dim3 grid = piece_grid(groups, pieces, kPieces * kThreads);
+  const bool four = four_pieces(groups, pieces);
+  const dim3 grid = piece_grid(groups, pieces, (four ? 4 : 1) * kThreads);
   auto go = [&](auto kern, auto* typed) {
     return launch_dependent(kern, grid, dim3(kThreads), 0, st, nullptr, 0, typed, tensor_scale, codes, scales, groups,
                             pieces);
   };
   const float* xf = static_cast<const float*>(x);
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
-  if (nv) return fp32 ? go(quantize_kernel<float, true>, xf) : go(quantize_kernel<__nv_bfloat16, true>, xb);
-  return fp32 ? go(quantize_kernel<float, false>, xf) : go(quantize_kernel<__nv_bfloat16, false>, xb);
+  using bf16 = __nv_bfloat16;
+  if (nv) {
+    if (fp32) return four ? go(quantize_kernel<float, true, 4>, xf) : go(quantize_kernel<float, true, 1>, xf);
+    return four ? go(quantize_kernel<bf16, true, 4>, xb) : go(quantize_kernel<bf16, true, 1>, xb);
+  }
+  if (fp32) return four ? go(quantize_kernel<float, false, 4>, xf) : go(quantize_kernel<float, false, 1>, xf);
+  return four ? go(quantize_kernel<bf16, false, 4>, xb) : go(quantize_kernel<bf16, false, 1>, xb);
 }
 
 cudaError_t launch_dequantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const uint8_t* codes,
                               const uint8_t* scales, const float* tensor_scale, void* out, cudaStream_t st) {
   const int64_t pieces = per_group / (fp32 ? 8 : 16);
-  const dim3 grid = piece_grid(groups, pieces, kPieces * kThreads);
+  const bool four = four_pieces(groups, pieces);
+  const dim3 grid = piece_grid(groups, pieces, (four ? 4 : 1) * kThreads);
   auto go = [&](auto kern, auto* typed) {
     return launch_dependent(kern, grid, dim3(kThreads), 0, st, nullptr, 0, codes, scales, tensor_scale, typed, groups,
                             pieces);
   };
   float* of = static_cast<float*>(out);
   __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(out);
-  if (nv) return fp32 ? go(dequantize_kernel<float, true>, of) : go(dequantize_kernel<__nv_bfloat16, true>, ob);
-  return fp32 ? go(dequantize_kernel<float, false>, of) : go(dequantize_kernel<__nv_bfloat16, false>, ob);
+  using bf16 = __nv_bfloat16;
+  if (nv) {
+    if (fp32) return four ? go(dequantize_kernel<float, true, 4>, of) : go(dequantize_kernel<float, true, 1>, of);
+    return four ? go(dequantize_kernel<bf16, true, 4>, ob) : go(dequantize_kernel<bf16, true, 1>, ob);
+  }
+  if (fp32) return four ? go(dequantize_kernel<float, false, 4>, of) : go(dequantize_kernel<float, false, 1>, of);
+  return four ? go(dequantize_kernel<bf16, false, 4>, ob) : go(dequantize_kernel<bf16, false, 1>, ob);
 }
 
 }  // namespace moe
