@@ -38,7 +38,7 @@ __device__ __forceinline__ void load_groups(RaggedGroups* g, const int32_t* grou
     const int64_t lo = offsets[e], hi = offsets[e + 1];
     const int64_t s = group_start != nullptr ? group_start[e] : lo;
     int64_t c = hi - lo;
-    if (c < 0 || s < 0 || s + c > rows) {
+    if (c < 0 || (c > 0 && (s < 0 || s + c > rows))) {  // (an empty group may start anywhere)
       report(status, DEV_BAD_GROUP);
       c = 0;
     }

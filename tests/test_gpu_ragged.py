@@ -164,6 +164,24 @@ def test_no_rows_at_all():
         assert torch.all(y == SENTINEL) and torch.all(dw == 0)
 
 
+def test_empty_groups_may_start_anywhere():
+    counts, n, k = [4, 0, 6, 0], 64, 64
+    gs, off, starts, total, x, dy, w, _ = make(counts, n, k, "gaps")
+    gs[1], gs[3] = -7, total + 1000
+    sh = M.grouped_shape(total, 4, n, k)
+    ws = M.grouped_workspace(sh)
+    y = torch.zeros(total, n, dtype=BF, device="cuda")
+    dw = torch.full((4, n, k), SENTINEL, dtype=BF, device="cuda")
+    M.moe_grouped_gemm(sh, x, gs, off, w, y, ws)
+    M.moe_grouped_gemm_wgrad(sh, dy, x, gs, off, dw, ws)
+    assert M.moe_get_device_status(ws) == 0
+    for e in (0, 2):
+        s, c = starts[e], counts[e]
+        xe, we = x[s:s + c].double(), w[e].double()
+        check(y[s:s + c], xe @ we.t(), xe.abs() @ we.abs().t(), k, f"y of expert {e}")
+    assert torch.all(dw[1] == 0) and torch.all(dw[3] == 0)
+
+
 def test_one_experts_nan_stays_with_it():
     """Groups end inside tiles: a neighbour's NaN rows are loaded and must not count."""
     counts, n, k = [5, 130, 7, 20], 72, 136
