@@ -14,20 +14,22 @@
 // scales are plain row-major bytes, so that a group may start at any row. TMA brings
 // 32 bytes of each row, the scales of two stages of 256 terms (NVFP4) or four (MXFP4),
 // and a warp per 128 rows turns its 4 KB round in place: 16-byte reads and stores, no
-// bank conflicts (32-byte swizzle). Loading them through registers instead is slow
-// (32768 rows
-// of 2048 x 2048: 227 us, 68 this way): the fence in front of the tensor core's reads waits for every load that the
-// warp has in flight. Only widths whose scale rows are no multiple of 16 bytes, which
-// TMA cannot address, go that way.
+// bank conflicts (32-byte swizzle; 16 bytes at a time TMA's own rate, about a row a
+// clock, was the bound). Only widths whose scale rows are no multiple of 16 bytes, which
+// TMA cannot address, go through registers (64 experts, 32768 rows of 2016: 127 us; of
+// 2048: 90): the fence in front of the tensor core's reads waits for every load that a
+// warp has in flight, so four sets of warps take the slots in turn (one set: 289).
 //
 // Structure per CTA (persistent, one an SM): warp 0 TMA of codes, warp 1 MMA issue,
-// warps 2..9 epilogue, the rest scale loaders. A 256-column accumulator pair and the
+// warps 2..9 epilogue, the rest scales. A 256-column accumulator pair and the
 // scales do not fit TMEM's 512 columns side by side, so the two accumulators share
 // 64 columns: the epilogue reads those first and then lets the next tile start.
 // PAIR: a tile of 256 output columns on the two CTAs of a cluster, each with its 128 rows
 // of the weight and half of the tile's rows in shared memory and the scales of its own
 // 128 weight rows and of all the tile's rows; the leader issues cta_group::2 copies and
-// MMAs for both.
+// MMAs for both (131072 rows, 64 experts: 338 us with one CTA a tile, 283 on pairs). What
+// bounds it is the tensor pipe's issue, 724 cycles a stage whose MMAs take 512, and next
+// to it the rate at which an SM's shared memory fills, 38 KB a stage.
 // The scale warps arrive on the leader's barrier without a cluster-scope release: each
 // CTA's lines are read from its own shared memory by its own tensor core (with one,
 // 32768 rows of 2048 x 2048 took 141 us instead of 86).
