@@ -520,9 +520,11 @@ def _arg(t, dtype, shape, name, device, allow_none=False):
     these takes up to ten tensors and a few microseconds); a wrong one is told by _ptr."""
     if t is None and allow_none:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == device):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _ptr(t, dtype, shape, name)
     raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
 
@@ -607,6 +609,9 @@ def moe_grouped_gemm_wgrad(shape, dy, x, group_start, offsets, dw, ws, stream=No
     _check(st, "moe_grouped_gemm_wgrad")
 
 
+_DTYPE_CODE = {torch.bfloat16: MOE_BF16, torch.float32: MOE_FP32}
+
+
 def _micro_block(fmt):
     if fmt not in MICRO_BLOCK:
         raise ValueError("format must be MOE_MXFP4 or MOE_NVFP4")
@@ -617,11 +622,13 @@ def _micro_shape(t, name):
     """[groups, rows, cols] of a matrix or a stack of matrices, and its dtype code."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() not in (2, 3):
+    shape = t.shape
+    if len(shape) not in (2, 3):
         raise ValueError(f"{name} must have two or three dimensions")
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    dt = _DTYPE_CODE.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return (1, *t.shape, int(t.dtype is torch.float32)) if t.dim() == 2 else (*t.shape, int(t.dtype is torch.float32))
+    return (1, shape[0], shape[1], dt) if len(shape) == 2 else (shape[0], shape[1], shape[2], dt)
 
 
 def _micro_args(fmt, t, name, tensor_scale, codes, scales, dev):
@@ -630,11 +637,12 @@ def _micro_args(fmt, t, name, tensor_scale, codes, scales, dev):
     G, R, K, dt = _micro_shape(t, name)
     if K % 32:
         raise ValueError(f"{name} must have a multiple of 32 columns, got {K}")
-    lead = t.shape[:-1]
-    return (G, R, K, dt, _arg(t, t.dtype, t.shape, name, dev),
+    shape = t.shape
+    lead = (R,) if len(shape) == 2 else (G, R)
+    return (G, R, K, dt, _arg(t, t.dtype, shape, name, dev),
             _arg(tensor_scale, torch.float32, (G,), "tensor_scale", dev, allow_none=True),
-            _arg(codes, torch.uint8, (*lead, K // 2), "codes", dev),
-            _arg(scales, torch.uint8, (*lead, K // block), "scales", dev))
+            _arg(codes, torch.uint8, lead + (K // 2,), "codes", dev),
+            _arg(scales, torch.uint8, lead + (K // block,), "scales", dev))
 
 
 def moe_tensor_scale_microscaled(x, scale, stream=None):

@@ -621,8 +621,8 @@ cudaError_t run_rows(const void* w, const void* x, const RArgs& a, cudaStream_t 
 constexpr int64_t kStageNs[kTileKinds] = {270, 290, 340, 475, 420};
 constexpr int64_t kPairStartNs = 2000;  // a cluster launch and its barriers
 
-int64_t turns_of(int kind, int64_t units) {
-  const int64_t slots = device_sm_count() / (kind == kTilePair ? 2 : 1);
+int64_t turns_of(int kind, int64_t units, int64_t sms) {
+  const int64_t slots = sms / (kind == kTilePair ? 2 : 1);
   return (units + slots - 1) / slots;
 }
 
@@ -630,13 +630,13 @@ int64_t turns_of(int kind, int64_t units) {
 // 64 columns) that ends first: its turns times a turn's stages and its stores.
 template <bool O32>
 cudaError_t run_weights(const void* dy, const void* x, const RArgs& a, cudaStream_t st) {
-  const int64_t stages = (a.rows / a.E + 63) / 64;
+  const int64_t stages = (a.rows / a.E + 63) / 64, sms = device_sm_count();
   int best = kTile64;
   int64_t least = INT64_MAX;
   for (int kind = kTile64; kind < kTileKinds; ++kind) {
     const int bm = kind == kTilePair ? 256 : 128, bn = kind == kTile64 ? 64 : kind == kTile128 ? 128 : 256;
     const int64_t units = static_cast<int64_t>(a.E) * ((a.n + bm - 1) / bm) * ((a.k + bn - 1) / bn);
-    const int64_t ns = turns_of(kind, units) * (stages * kStageNs[kind] + 700 + 8 * bn) +
+    const int64_t ns = turns_of(kind, units, sms) * (stages * kStageNs[kind] + 700 + 8 * bn) +
                        (kind == kTilePair ? kPairStartNs : 0);
     if (ns < least) {
       least = ns;
@@ -661,7 +661,7 @@ cudaError_t run_weights(const void* dy, const void* x, const RArgs& a, cudaStrea
 // against 106 with 256 rows); a single group of 96 rows takes 32 so that more SMs read
 // its weight.
 int pick_row_tile(int64_t rows, int E, int out_cols, int64_t stages, int stage_percent) {
-  const int64_t groups = rows < E ? rows : E;
+  const int64_t groups = rows < E ? rows : E, sms = device_sm_count();
   const int64_t mean = (rows + groups - 1) / groups;
   const int64_t tall = mean + 2 * static_cast<int64_t>(std::sqrt(static_cast<double>(mean)));
   int best = kTile32;
@@ -669,7 +669,7 @@ int pick_row_tile(int64_t rows, int E, int out_cols, int64_t stages, int stage_p
   for (int kind = kTile32; kind < kTileKinds; ++kind) {
     const int bm = kind == kTilePair ? 256 : 128, most = kind == kTilePair ? 256 : 32 << kind;
     const int64_t units = groups * ((tall + most - 1) / most) * ((out_cols + bm - 1) / bm);
-    const int64_t ns = turns_of(kind, units) * (stages * kStageNs[kind] * stage_percent / 100 + 600) +
+    const int64_t ns = turns_of(kind, units, sms) * (stages * kStageNs[kind] * stage_percent / 100 + 600) +
                        (kind == kTilePair ? kPairStartNs : 0);
     if (ns < least) {
       least = ns;
