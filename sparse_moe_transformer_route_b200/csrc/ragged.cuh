@@ -1,5 +1,5 @@
 // Shared by the ragged grouped products: the checked group layout in shared memory,
-// the tile schedule, the issue of MMAs, and the masked stores of an accumulator chunk.
+// the tile schedule, the issue of MMAs, and the masked store of an accumulator chunk.
 #pragma once
 
 #include <type_traits>
@@ -205,52 +205,6 @@ __device__ __forceinline__ void store_chunk_turned(const float (&v)[32], T* g, i
       if (j < mine) *reinterpret_cast<uint32_t*>(p) = w;
       p += 2 * ld;
     }
-  }
-}
-
-// One warp writes a 32 x 32 chunk whose row `lane` this thread holds in v, through
-// a staging buffer of 32 rows of PITCH bytes so that each store instruction covers
-// whole row pieces. Only the first `rows` rows and `cols` columns (a multiple of 8)
-// are written; rows past a group's end belong to another group or to nobody.
-template <typename T, int PITCH>
-__device__ __forceinline__ void store_chunk_masked(unsigned char* stg, const float (&v)[32], T* g, int64_t ld, int rows,
-                                                   int cols, int lane) {
-  constexpr int CPP = (PITCH - 16) / static_cast<int>(sizeof(T));  // columns a pass
-  static_assert(CPP == 32 || CPP == 16 || CPP == 8, "pitch");
-  constexpr int RB = CPP * static_cast<int>(sizeof(T));
-  constexpr int LPR = RB / 16;   // lanes a row on the way out
-  constexpr int RPI = 32 / LPR;  // rows a store instruction
-  constexpr int EPS = 16 / static_cast<int>(sizeof(T));  // elements of a 16-byte piece
-  unsigned char* mine = stg + lane * PITCH;
-#pragma unroll
-  for (int p = 0; p < 32 / CPP; ++p) {
-    if constexpr (std::is_same_v<T, float>) {
-#pragma unroll
-      for (int i = 0; i < CPP / 4; ++i)
-        *reinterpret_cast<float4*>(mine + 16 * i) =
-            make_float4(v[p * CPP + 4 * i], v[p * CPP + 4 * i + 1], v[p * CPP + 4 * i + 2], v[p * CPP + 4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < CPP / 8; ++i) {
-        const int b = p * CPP + 8 * i;
-        uint4 w;
-        w.x = pack_bf16x2(v[b], v[b + 1]);
-        w.y = pack_bf16x2(v[b + 2], v[b + 3]);
-        w.z = pack_bf16x2(v[b + 4], v[b + 5]);
-        w.w = pack_bf16x2(v[b + 6], v[b + 7]);
-        *reinterpret_cast<uint4*>(mine + 16 * i) = w;
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int it = 0; it < 32 / RPI; ++it) {
-      const int r = it * RPI + lane / LPR;
-      const int seg = lane % LPR;
-      const uint4 val = *reinterpret_cast<const uint4*>(stg + r * PITCH + seg * 16);
-      if (r < rows && p * CPP + seg * EPS < cols)
-        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(g + r * ld + p * CPP) + seg * 16) = val;
-    }
-    __syncwarp();
   }
 }
 

@@ -4,7 +4,7 @@
 // and a weight W_e [n, k]:
 //   forward   y[r]  = W_e x[r]                        Y_e^T  = W_e   X_e^T
 //   dgrad     dx[r] = W_e^T dy[r]                     dX_e^T = W_e^T dY_e^T
-//   wgrad     dW_e  = sum over rows r of dy[r] x[r]^T dW_e   = dY_e^T X_e
+//   wgrad     dW_e  = sum over rows r of dy[r] x[r]^T dW_e^T = X_e^T dY_e
 // bf16 operands, fp32 sums, bf16 or fp32 results.
 //
 // Sizes. Forward and dgrad make the weight the MMA's M operand (128 output columns a
@@ -64,8 +64,8 @@ struct RCfg {
   static constexpr int CTAS = PAIR ? 2 : 1;
   static constexpr bool A_MN = OP != Op::Fwd;  // operand read as [reduction][row of the operand]
   static constexpr bool B_MN = W;
-  static constexpr int BM = 128 * CTAS;        // M: output columns (fwd, dgrad), rows of dW
-  static constexpr int BN = BN_;               // N: at most so many rows (fwd, dgrad), columns of dW
+  static constexpr int BM = 128 * CTAS;        // M: columns of the result
+  static constexpr int BN = BN_;               // N: at most so many of its rows
   static constexpr int UNIT = 16 * CTAS;       // N is a multiple of this
   static constexpr int B_ROWS = BN / CTAS;     // of the N operand in this CTA's shared memory
   static constexpr bool O32 = O32_;
@@ -91,13 +91,10 @@ struct RCfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int CHUNKS = (BN + 63) / 64;  // 32-column accumulator chunks of an epilogue warp
-  static constexpr int STG_PITCH = 32 * 2 + 16;  // wgrad; fp32 leaves in two passes
-  static constexpr int STG_WARP_BYTES = W ? 32 * STG_PITCH : 0;
-  static constexpr int STG_BYTES = EPI_WARPS * STG_WARP_BYTES;
   static constexpr int MISC_BYTES = 1024 + static_cast<int>(sizeof(RaggedGroups));
-  static constexpr int STAGES_FIT = (227 * 1024 - 1024 - MISC_BYTES - STG_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES_FIT = (227 * 1024 - 1024 - MISC_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_FIT > 12 ? 12 : STAGES_FIT;
-  static constexpr size_t SMEM_BYTES = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + STG_BYTES + MISC_BYTES;
+  static constexpr size_t SMEM_BYTES = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + MISC_BYTES;
   static_assert(STAGES >= 4 && (3 * STAGES + 7) * 8 <= 1024, "ring");
   static_assert(BN == 256 || (!PAIR && (BN == 128 || BN == 64 || (BN == 32 && !W))), "tile N");
   // no two CTAs of such kernels share an SM: one that is launched early (as a dependent)
@@ -116,24 +113,24 @@ struct RArgs {
 
 struct RTile {
   int e;
-  int m0;   // first row of the M operand: output column (fwd, dgrad), row of dW_e
-  int n0;   // first row of the N operand: row of the buffer (fwd, dgrad), column of dW_e
+  int m0;   // first column of the result
+  int n0;   // its first row: of the buffer (fwd, dgrad) or of dW_e
   int N;    // the MMA's N
   int red;  // length of the reduction
   int row0; // wgrad: first row of the group
-  int left; // rows of the N operand that exist (fwd, dgrad: rows of the group, at most N)
+  int left; // rows that exist (fwd, dgrad: of the group, at most N)
 };
 
 template <class C>
 struct Schedule {
   int n_tiles, nM, m_size, c, G;
-  __device__ static int m_tiles(const RArgs& a) { return ((C::OP == Op::Dgrad ? a.k : a.n) + C::BM - 1) / C::BM; }
+  __device__ static int m_tiles(const RArgs& a) { return ((C::OP == Op::Fwd ? a.n : a.k) + C::BM - 1) / C::BM; }
   __device__ Schedule(const RArgs& a, const RaggedGroups& g) {
     c = static_cast<int>(blockIdx.x) / C::CTAS;
     G = static_cast<int>(gridDim.x) / C::CTAS;
-    m_size = C::OP == Op::Dgrad ? a.k : a.n;
+    m_size = C::OP == Op::Fwd ? a.n : a.k;
     nM = m_tiles(a);
-    n_tiles = C::W ? a.E * nM * ((a.k + C::BN - 1) / C::BN) : g.tiles[a.E];
+    n_tiles = C::W ? a.E * nM * ((a.n + C::BN - 1) / C::BN) : g.tiles[a.E];
   }
   // Tile of this CTA's (pair's) turn i, or -1. wgrad's tiles cost their group's rows and
   // come largest group first: every other turn runs backwards over the CTAs, which evens
@@ -147,7 +144,7 @@ struct Schedule {
   __device__ RTile tile(const RArgs& a, const RaggedGroups& g, int L) const {
     RTile t;
     if constexpr (C::W) {
-      const int nN = (a.k + C::BN - 1) / C::BN;
+      const int nN = (a.n + C::BN - 1) / C::BN;
       const int mt = L / nN;
       t.n0 = (L - mt * nN) * C::BN;
       t.e = g.order[mt / nM];
@@ -155,7 +152,7 @@ struct Schedule {
       t.N = C::BN;
       t.red = g.count[t.e];
       t.row0 = g.start[t.e];
-      t.left = a.k - t.n0;
+      t.left = a.n - t.n0;
     } else {
       const int place = tile_place(g, a.E, L);
       t.e = g.order[place];
@@ -194,15 +191,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* stg_base = smem + static_cast<size_t>(C::STAGES) * C::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stg_base + C::STG_BYTES);
+  unsigned char* misc = smem + static_cast<size_t>(C::STAGES) * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint64_t* ragged_full = drain + 1;  // per stage: the peer's copies of a group's last, ragged stage (wgrad)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ragged_full + C::STAGES);
-  RaggedGroups* groups = reinterpret_cast<RaggedGroups*>(stg_base + C::STG_BYTES + 1024);
+  RaggedGroups* groups = reinterpret_cast<RaggedGroups*>(misc + 1024);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -456,7 +453,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     using OutT = typename C::OutT;
     const int q = warp & 3;               // TMEM lane quarter of this warp
     const int csel = (warp - 2) >> 2;     // it takes every other 32-column chunk
-    unsigned char* stg = stg_base + (warp - 2) * C::STG_WARP_BYTES;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -484,13 +480,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
       // one 32 x 32 chunk, accumulator columns [c, c + 32)
       auto store = [&](const float (&v)[32], int c) {
-        if constexpr (C::W) {
-          OutT* out = static_cast<OutT*>(a.out) + (static_cast<int64_t>(t.e) * a.n + mrow) * a.k + t.n0 + c;
-          store_chunk_masked<OutT, C::STG_PITCH>(stg, v, out, a.k, m_left, t.left - c, lane);
-        } else {
-          OutT* out = static_cast<OutT*>(a.out) + (static_cast<int64_t>(t.n0) + c) * sched.m_size + mrow;
-          store_chunk_turned<OutT>(v, out, sched.m_size, t.left - c, m_left, lane);
-        }
+        const int64_t row = (C::W ? static_cast<int64_t>(t.e) * a.n : 0) + t.n0 + c;
+        OutT* out = static_cast<OutT*>(a.out) + row * sched.m_size + mrow;
+        store_chunk_turned<OutT>(v, out, sched.m_size, t.left - c, m_left, lane);
       };
       if constexpr (C::PARTS) {
         float sum[C::CHUNKS * 32];
@@ -579,10 +571,10 @@ cudaError_t launch(const void* A, const void* B, const RArgs& a, cudaStream_t st
   CUtensorMap ta, tb, tb32;
   int64_t tiles;
   if (OP == Op::Wgrad) {
-    if (!make_map(&ta, A, false, rows, n, 64, 64) || !make_map(&tb, B, false, rows, k, 64, 64))
+    if (!make_map(&ta, A, false, rows, k, 64, 64) || !make_map(&tb, B, false, rows, n, 64, 64))
       return cudaErrorInvalidValue;
     tb32 = tb;
-    tiles = static_cast<int64_t>(a.E) * ((a.n + C::BM - 1) / C::BM) * ((a.k + BN - 1) / BN);
+    tiles = static_cast<int64_t>(a.E) * ((a.k + C::BM - 1) / C::BM) * ((a.n + BN - 1) / BN);
   } else {
     const uint64_t width = OP == Op::Fwd ? k : n;
     if (!make_map_3d(&ta, A, static_cast<uint64_t>(a.E), n, k, 64, OP == Op::Fwd ? 128 : 64) ||
@@ -626,8 +618,8 @@ int64_t turns_of(int kind, int64_t units, int64_t sms) {
   return (units + slots - 1) / slots;
 }
 
-// dW: the kind of tile (256 rows of dW by 256 columns on a pair, or 128 rows by 256, 128 or
-// 64 columns) that ends first: its turns times a turn's stages and its stores.
+// dW: the kind of tile (256 columns of dW by 256 rows on a pair, or 128 columns by 256, 128
+// or 64 rows) that ends first: its turns times a turn's stages and its stores.
 template <bool O32>
 cudaError_t run_weights(const void* dy, const void* x, const RArgs& a, cudaStream_t st) {
   const int64_t stages = (a.rows / a.E + 63) / 64, sms = device_sm_count();
@@ -635,7 +627,7 @@ cudaError_t run_weights(const void* dy, const void* x, const RArgs& a, cudaStrea
   int64_t least = INT64_MAX;
   for (int kind = kTile64; kind < kTileKinds; ++kind) {
     const int bm = kind == kTilePair ? 256 : 128, bn = kind == kTile64 ? 64 : kind == kTile128 ? 128 : 256;
-    const int64_t units = static_cast<int64_t>(a.E) * ((a.n + bm - 1) / bm) * ((a.k + bn - 1) / bn);
+    const int64_t units = static_cast<int64_t>(a.E) * ((a.k + bm - 1) / bm) * ((a.n + bn - 1) / bn);
     const int64_t ns = turns_of(kind, units, sms) * (stages * kStageNs[kind] + 700 + 8 * bn) +
                        (kind == kTilePair ? kPairStartNs : 0);
     if (ns < least) {
@@ -644,10 +636,10 @@ cudaError_t run_weights(const void* dy, const void* x, const RArgs& a, cudaStrea
     }
   }
   switch (best) {
-    case kTilePair: return launch<Op::Wgrad, 256, true, O32>(dy, x, a, st);
-    case kTile256: return launch<Op::Wgrad, 256, false, O32>(dy, x, a, st);
-    case kTile128: return launch<Op::Wgrad, 128, false, O32>(dy, x, a, st);
-    default: return launch<Op::Wgrad, 64, false, O32>(dy, x, a, st);
+    case kTilePair: return launch<Op::Wgrad, 256, true, O32>(x, dy, a, st);
+    case kTile256: return launch<Op::Wgrad, 256, false, O32>(x, dy, a, st);
+    case kTile128: return launch<Op::Wgrad, 128, false, O32>(x, dy, a, st);
+    default: return launch<Op::Wgrad, 64, false, O32>(x, dy, a, st);
   }
 }
 
