@@ -166,15 +166,14 @@ struct QTile {
 };
 
 template <class C>
-__device__ __forceinline__ QTile q_tile(const QArgs& a, const RaggedGroups& g, int nM, int L) {
+__device__ __forceinline__ QTile q_tile(const QArgs& a, const RaggedGroups& g, const FastDiv& by_m, int L) {
   QTile t;
   const int place = tile_place(g, a.E, L);
   t.e = g.order[place];
   const int in = L - g.tiles[place];
-  const int rt = in / nM;
-  t.m0 = (in - rt * nM) * C::BM;
-  const int count = g.count[t.e];
-  const int per = rows_a_tile<C::BN, C::UNIT>(count);
+  const int rt = by_m(in);
+  t.m0 = (in - rt * static_cast<int>(by_m.d)) * C::BM;
+  const int count = g.count[t.e], per = g.per[t.e];
   t.n0 = g.start[t.e] + rt * per;
   t.left = min(per, count - rt * per);
   t.N = (t.left + C::UNIT - 1) / C::UNIT * C::UNIT;
@@ -296,8 +295,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
   __syncwarp();
   pdl_wait();
-  const int nM = (a.n + C::BM - 1) / C::BM;
-  load_groups<C::BN, C::UNIT, false>(groups, a.group_start, a.offsets, a.E, a.rows, nM, a.status);
+  const FastDiv by_m((a.n + C::BM - 1) / C::BM);
+  load_groups<C::BN, C::UNIT, false>(groups, a.group_start, a.offsets, a.E, a.rows, static_cast<int>(by_m.d), a.status);
   tc_fence_before();
   if constexpr (C::PAIR)
     cluster_sync_all();
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     int issued = 0;
     bool ok = true;
     for (int L = first_tile; L < n_tiles && ok; L += grid) {
-      const QTile t = q_tile<C>(a, *groups, nM, L);
+      const QTile t = q_tile<C>(a, *groups, by_m, L);
       // few rows: 32-row boxes over those that count
       const int need = uniform(t.N) / CTAS;
       const int boxes = need > C::B_ROWS - 32 ? 0 : (need + 31) / 32;
@@ -391,7 +390,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           break;
         }
         const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
-        const uint32_t n_bits = uniform(static_cast<uint32_t>(q_tile<C>(a, *groups, nM, L).N) >> 3 << 17);
+        const uint32_t n_bits = uniform(static_cast<uint32_t>(q_tile<C>(a, *groups, by_m, L).N) >> 3 << 17);
         for (int kb = 0; kb < nk; ++kb) {
           const int sub = kb % C::SF_STAGES_PER;
           if (!__all_sync(0xffffffffu,
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int csel = (warp - 2) >> 2;
     int tile = 0;
     for (int L = first_tile; L < n_tiles; L += grid, ++tile) {
-      const QTile t = q_tile<C>(a, *groups, nM, L);
+      const QTile t = q_tile<C>(a, *groups, by_m, L);
       const int acc = tile & 1;
       float alpha = 1.0f;
       if (a.x_scale != nullptr) alpha = __ldg(a.x_scale);
@@ -502,7 +501,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             if constexpr (C::PAIR)
-              mbar_arrive_cluster(acc_empty_leader);
+              mbar_arrive_cluster_relaxed(acc_empty_leader);
             else
               mbar_arrive(&acc_empty[C::OVERLAP ? 0 : acc]);
           }
@@ -555,7 +554,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int issued = 0;
         bool ok = true;
         for (int L = first_tile; L < n_tiles && ok; L += grid) {
-          const QTile t = q_tile<C>(a, *groups, nM, L);
+          const QTile t = q_tile<C>(a, *groups, by_m, L);
           const int rows = uniform(t.N);
           const int boxes = rows > C::BN - 32 ? 0 : (rows + 31) / 32;
           const uint32_t bytes = static_cast<uint32_t>(32 * (128 + (boxes == 0 ? C::BN : 32 * boxes)));
@@ -621,7 +620,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       bool live[4];
       auto aim = [&]() {
         if (lL >= n_tiles) return;
-        const QTile t = q_tile<C>(a, *groups, nM, lL);
+        const QTile t = q_tile<C>(a, *groups, by_m, lL);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = lane + 32 * i;

@@ -124,8 +124,10 @@ struct RTile {
 template <class C>
 struct Schedule {
   int n_tiles, nM, m_size, c, G;
+  FastDiv by_m, by_n;  // (by_n: wgrad)
   __device__ static int m_tiles(const RArgs& a) { return ((C::OP == Op::Fwd ? a.n : a.k) + C::BM - 1) / C::BM; }
-  __device__ Schedule(const RArgs& a, const RaggedGroups& g) {
+  __device__ Schedule(const RArgs& a, const RaggedGroups& g)
+      : by_m(m_tiles(a)), by_n(C::W ? (a.n + C::BN - 1) / C::BN : 1) {
     c = static_cast<int>(blockIdx.x) / C::CTAS;
     G = static_cast<int>(gridDim.x) / C::CTAS;
     m_size = C::OP == Op::Fwd ? a.n : a.k;
@@ -144,11 +146,11 @@ struct Schedule {
   __device__ RTile tile(const RArgs& a, const RaggedGroups& g, int L) const {
     RTile t;
     if constexpr (C::W) {
-      const int nN = (a.n + C::BN - 1) / C::BN;
-      const int mt = L / nN;
-      t.n0 = (L - mt * nN) * C::BN;
-      t.e = g.order[mt / nM];
-      t.m0 = (mt % nM) * C::BM;
+      const int mt = by_n(L);
+      t.n0 = (L - mt * static_cast<int>(by_n.d)) * C::BN;
+      const int place = by_m(mt);
+      t.e = g.order[place];
+      t.m0 = (mt - place * nM) * C::BM;
       t.N = C::BN;
       t.red = g.count[t.e];
       t.row0 = g.start[t.e];
@@ -157,10 +159,9 @@ struct Schedule {
       const int place = tile_place(g, a.E, L);
       t.e = g.order[place];
       const int in = L - g.tiles[place];
-      const int rt = in / nM;
+      const int rt = by_m(in);
       t.m0 = (in - rt * nM) * C::BM;
-      const int count = g.count[t.e];
-      const int per = rows_a_tile<C::BN, C::UNIT>(count);
+      const int count = g.count[t.e], per = g.per[t.e];
       t.n0 = g.start[t.e] + rt * per;
       t.left = min(per, count - rt * per);
       t.N = (t.left + C::UNIT - 1) / C::UNIT * C::UNIT;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         if constexpr (C::PAIR)
-          mbar_arrive_cluster(acc_empty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+          mbar_arrive_cluster_relaxed(acc_empty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
         else
           mbar_arrive(&acc_empty[acc]);
       }
