@@ -27,9 +27,10 @@
 // PAIR: a tile of 256 output columns on the two CTAs of a cluster, each with its 128 rows
 // of the weight and half of the tile's rows in shared memory and the scales of its own
 // 128 weight rows and of all the tile's rows; the leader issues cta_group::2 copies and
-// MMAs for both (131072 rows, 64 experts: 338 us with one CTA a tile, 283 on pairs). What
-// bounds it is the tensor pipe's issue, 724 cycles a stage whose MMAs take 512, and next
-// to it the rate at which an SM's shared memory fills, 38 KB a stage.
+// MMAs for both (131072 rows, 64 experts: 338 us with one CTA a tile, 283 on pairs, 266
+// with the accumulator's release relaxed and shorter tile lookups). What bounds it is the
+// operands' way into shared memory: 38 KB a stage whose MMAs take 512 cycles, five
+// stages in flight, about 2 us from a stage's release to its next use.
 // The scale warps arrive on the leader's barrier without a cluster-scope release: each
 // CTA's lines are read from its own shared memory by its own tensor core (with one,
 // 32768 rows of 2048 x 2048 took 141 us instead of 86).
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if constexpr (C::PAIR)
               mbar_arrive_cluster_relaxed(acc_empty_leader);
             else
-              mbar_arrive(&acc_empty[C::OVERLAP ? 0 : acc]);
+              mbar_arrive_relaxed(&acc_empty[C::OVERLAP ? 0 : acc]);
           }
         }
         if (c < t.N) {

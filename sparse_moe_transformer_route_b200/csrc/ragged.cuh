@@ -20,9 +20,9 @@ struct RaggedGroups {
   int32_t tiles[kMaxExperts + 1];
 };
 
-// Every warp works out each of its tiles: the integer divisions and the search of a plain
-// version took 1850 cycles a tile, as long as a short reduction's whole tile (54425 rows
-// of 120 over 51 experts, 1432 wide: 57 us, FASTER us with what follows).
+// Every warp works out each of its tiles by itself, so divisions go by multiplication
+// and the search is one of the whole warp (131072 rows of 4-bit values over 64 experts:
+// 283 us with plain divisions and a binary search, 274 so).
 
 // x / d for 0 <= x < 2^31 by a multiplication.
 struct FastDiv {
@@ -197,17 +197,22 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint64_
 
 // Arrival on another CTA's barrier by an epilogue warp that has read its accumulator. It
 // orders TMEM reads only (tcgen05.wait::ld and the fence before it do), so it is relaxed:
-// a releasing one waits until the warp's stores to global memory have been performed.
+// a releasing one waits until the warp's stores to global memory have been performed
+// (131072 rows over 64 experts: gradients 1.70 -> 1.65 ms, the 4-bit product 274 -> 266 us).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // One warp writes a 32 x 32 chunk whose COLUMN `lane` this thread holds in v: v[j] is
 // the element of row j. fp32 rows leave as 128 bytes a store; bf16 neighbours swap one
 // of every two rows, packed, and two rows of 64 bytes leave a store. Only the first
 // `rows` rows and `cols` columns (a multiple of 8) are written. Short reductions are
-// bound by these instructions (54425 rows of 120 over 51 experts, 1432 wide: 59 us
-// with values swapped before they are packed and every store predicated, FASTER so).
+// bound by this (54425 rows of 120 over 51 experts, 1432 wide: 59 us with values swapped
+// before they are packed and every store predicated, 57 so).
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void store_columns(const float (&v)[32], T* g, int64_t ld, int rows, int cols, int lane) {
   if constexpr (std::is_same_v<T, float>) {

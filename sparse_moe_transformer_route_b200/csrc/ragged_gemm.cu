@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (C::PAIR)
           mbar_arrive_cluster_relaxed(acc_empty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
         else
-          mbar_arrive(&acc_empty[acc]);
+          mbar_arrive_relaxed(&acc_empty[acc]);
       }
       if (++acc == 2) {
         acc = 0;
