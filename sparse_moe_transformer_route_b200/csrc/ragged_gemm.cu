@@ -28,8 +28,8 @@
 // Every wait is bounded; a timeout is recorded in the status word and the CTA unwinds.
 // What bounds it: few rows, the stream of weights (64 rows over 64 experts of 2048 x
 // 2048: 55 us, 92% of the measured HBM rate); many, the tensor cores (one expert of
-// 32768 rows 164 us, 1,680 TFLOP/s; 131072 rows over 64 experts: dgrad 742 us, wgrad,
-// which also writes 1 GB of fp32, 915 us).
+// 32768 rows 164 us, 1,680 TFLOP/s; 131072 rows over 64 experts: dgrad and wgrad,
+// which also writes 1 GB of fp32, 1.65 ms together; under a lasting load the power cap).
 //
 // PAIR: a tile is 256 x BN on the two CTAs of a cluster (the SMs of one TPC), each with
 // its 128 rows of the M operand, half of the N operand and its 128 accumulator rows;
