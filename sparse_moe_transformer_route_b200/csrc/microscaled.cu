@@ -347,6 +347,10 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ uint32_t warp_top[kThreads / 32];
   __shared__ uint32_t cta_top[kMaxCluster];
   pdl_trigger();
+  // A CTA's shared memory may be written by another only once it is known to have
+  // started: each tells the cluster here and waits for the others before its first result
+  // leaves, after the loads (a CTA whose share of the group is empty gets there at once).
+  if constexpr (CLUSTER) cluster_arrive();
   pdl_wait();
   const bool wide = aligned32(x);
   for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
@@ -389,6 +393,10 @@ __global__ void __launch_bounds__(kThreads)
       mine = __float_as_uint(fmaxf(__uint_as_float(top) / 2688.0f, kMinTensorScale));
     }
     if constexpr (CLUSTER) {
+      if (grp == blockIdx.y) {  // the first of this cluster's groups
+        __syncwarp();
+        cluster_wait();
+      }
       if (threadIdx.x == 0) {
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&cta_top[blockIdx.x]), 0)), "r"(mine)
                      : "memory");
