@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* drain = acc_empty + 2;
   uint64_t* ragged_full = drain + 1;  // per stage: the peer's copies of a group's last, ragged stage (wgrad)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ragged_full + C::STAGES);
+  volatile uint32_t* loads = tmem_holder + 1;  // stages that this CTA's producer has asked for (wgrad on a pair)
   RaggedGroups* groups = reinterpret_cast<RaggedGroups*>(misc + 1024);
 
   const int warp = threadIdx.x >> 5;
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     mbar_init(drain, 1);
     fence_mbar_init();
+    *loads = 0;
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
@@ -303,6 +305,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             load(&tmA, sa + C::CHUNK_BYTES, am + 64);
 #pragma unroll
             for (int ch = 0; ch < C::B_ROWS / 64; ++ch) load(&tmB, sb + ch * C::CHUNK_BYTES, bn + ch * 64);
+            if constexpr (C::PAIR) *loads = static_cast<uint32_t>(issued + 1);
           } else {
             auto load_w = [&](unsigned char* dst, int c0, int c1) {
               if constexpr (C::PAIR)
@@ -431,11 +434,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int nk = (t.red + C::BK - 1) / C::BK;
         if (t.red % C::UK != 0) {
           const int last = (stage + nk - 1) % C::STAGES;
-          // the stage is loaded after the whole group before it: one bounded wait for
-          // every 2^18 rows, each a small part of a second's work
+          // The stage is loaded after everything before it, any number of tiles: the wait
+          // goes on for as long as this CTA's producer does, each of whose own waits is
+          // bounded, and gives up when it has asked for nothing new in a whole bounded wait.
           bool in = false;
-          for (int w = 0; w <= nk / 4096 && !in; ++w)
+          uint32_t before, now = uniform(*loads);
+          do {
+            before = now;
             in = __all_sync(0xffffffffu, mbar_wait(&ragged_full[last], (parity >> last) & 1u));
+            now = uniform(*loads);
+          } while (!in && now != before);
           if (!in) {
             if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_MMA);
             break;
