@@ -458,7 +458,9 @@ moe_status moe_dequantize_microscaled(int32_t format, int64_t groups, int64_t ro
  *   x_scale [device] [1] fp32 or NULL for 1
  *   w_codes [device] [n_experts, n, k / 2], w_scales [device] [n_experts, n, k / 32 or / 16],
  *   w_scale [device] [n_experts] fp32 or NULL for 1 (both NULL for MOE_MXFP4)
- *   the others as for moe_grouped_gemm. */
+ *   the others as for moe_grouped_gemm.
+ * Tensor scales in [2^-100, 2^117], as the conversions take them: the result is then
+ * 0, infinite or subnormal only where the product of the sum and both scales is. */
 moe_status moe_grouped_gemm_microscaled(const moe_grouped_shape* shape, int32_t format, const uint8_t* x_codes,
                                         const uint8_t* x_scales, const float* x_scale, const int32_t* group_start,
                                         const int32_t* offsets, const uint8_t* w_codes, const uint8_t* w_scales,

@@ -76,7 +76,7 @@ struct QCfg {
   static constexpr int SF_SETS = 4;
   static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_SETS * SF_WARPS + 1);
   static constexpr int CHUNKS = (BN + 63) / 64;  // 32-column chunks of an epilogue warp
-  static constexpr int MISC_BYTES = 1024 + static_cast<int>(sizeof(RaggedGroups));
+  static constexpr int MISC_BYTES = 1024 + static_cast<int>(sizeof(RaggedGroups)) + 4 * kMaxExperts;
   static constexpr int ROOM = 227 * 1024 - 1024 - MISC_BYTES;
   static constexpr int STAGES_FIT = (ROOM - 4 * SF_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
@@ -87,7 +87,7 @@ struct QCfg {
   static constexpr int SF_SLOTS = (SF_FIT > 8 ? 8 : SF_FIT) / SF_SETS * SF_SETS;
   static constexpr size_t SMEM_BYTES =
       1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + static_cast<size_t>(SF_SLOTS) * SF_BYTES + MISC_BYTES;
-  static_assert(STAGES >= 3 && SF_SLOTS >= 4 && SF_SLOTS % SF_SETS == 0 && (2 * STAGES + 3 * SF_SLOTS + 6) * 8 <= 1024, "rings");
+  static_assert(STAGES >= 3 && SF_SLOTS >= 4 && SF_SLOTS % SF_SETS == 0 && (2 * STAGES + 3 * SF_SLOTS + 6) * 8 <= 1024 && THREADS >= kMaxExperts, "rings");
   static_assert(SMEM_BYTES > 114 * 1024, "one CTA an SM");
   static_assert(SFB_COL + WORDS * 4 * BBLK <= 512, "TMEM columns");
   static_assert(BN == 256 || (!PAIR && (BN == 128 || BN == 64 || BN == 32)), "tile N");
@@ -181,6 +181,47 @@ __device__ __forceinline__ QTile q_tile(const QArgs& a, const RaggedGroups& g, c
   return t;
 }
 
+// The product of the two tensor scales as shift * lead, which multiply a sum in this order.
+// Each scale may be anywhere in [2^-100, 2^117], so their product may leave fp32's normal
+// range although its product with a sum does not (a sum of products of 4-bit values and
+// block scales is 0 or at least 2^-20). It is then split in the middle, shift a power of
+// two: sum * shift is exact, or overflows where the whole does, and * lead rounds once.
+// Elsewhere lead is the rounded product and shift is 1.
+struct TensorScales {
+  float shift, lead;
+};
+
+__device__ __forceinline__ TensorScales tensor_scales(float gx, float gw) {
+  const float m = fabsf(gx * gw);
+  const bool normal = m >= 0x1p-126f && m <= 0x1.fffffep127f;
+  if (normal || gx == 0.0f || gw == 0.0f || !isfinite(gx) || !isfinite(gw)) return {1.0f, gx * gw};
+  int ex, ew;
+  const float f = frexpf(gx, &ex) * frexpf(gw, &ew);  // rounded once, as the product above
+  const int half = (ex + ew) / 2;
+  return {ldexpf(1.0f, ex + ew - half), ldexpf(f, half)};
+}
+
+// Multiplies this warp's chunks of an accumulator by `shift` where they are, in TMEM. A
+// second product for every element instead costs large products 3% (131072 rows of 2048 x
+// 2048 over 64 experts: 268 and 276 us), a second loop for such tiles needs more registers
+// than there are, and forming both factors a tile at a time costs 1.7%; every expert's
+// lead is formed once a CTA and lies in shared memory (0.8%).
+__device__ __forceinline__ void shift_chunks(uint32_t tb, int csel, int N, float shift) {
+#pragma unroll 1
+  for (int c = csel * 32; c < N; c += 64) {
+#pragma unroll 1
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t r[16];
+      tmem_ld16(tb + c + h, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * shift);
+      tmem_st16(tb + c + h, r);
+    }
+  }
+  tmem_st_wait();
+}
+
 // Eight words of a scale row from byte `at` on, zero past the row's end. The row starts
 // at any address: the (up to three) 16-byte pieces that cover the words are read whole
 // and shifted together, but for one that would leave the buffer at `end`, which is read
@@ -249,7 +290,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* far_flag = tmem_holder + 1;  // some expert's tensor scales have a shift
   RaggedGroups* groups = reinterpret_cast<RaggedGroups*>(misc + 1024);
+  float* lead = reinterpret_cast<float*>(groups + 1);  // of every expert's tensor scales
 
   constexpr int CTAS = C::CTAS;
   const int warp = threadIdx.x >> 5;
@@ -274,6 +317,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     mbar_init(drain, 1);
     fence_mbar_init();
+    *far_flag = 0;
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
@@ -297,7 +341,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncwarp();
   pdl_wait();
   const FastDiv by_m((a.n + C::BM - 1) / C::BM);
+  float gx = 1.0f, gw = 1.0f;  // a thread an expert, asked for ahead of the groups
+  if constexpr (C::NV) {
+    if (a.x_scale != nullptr) gx = __ldg(a.x_scale);
+    if (a.w_scale != nullptr && threadIdx.x < static_cast<unsigned>(a.E)) gw = __ldg(a.w_scale + threadIdx.x);
+  }
   load_groups<C::BN, C::UNIT, false>(groups, a.group_start, a.offsets, a.E, a.rows, static_cast<int>(by_m.d), a.status);
+  if (C::NV && threadIdx.x < static_cast<unsigned>(a.E)) {
+    const TensorScales by = tensor_scales(gx, gw);
+    lead[threadIdx.x] = by.lead;
+    if (by.shift != 1.0f) *far_flag = 1;
+  }
   tc_fence_before();
   if constexpr (C::PAIR)
     cluster_sync_all();
@@ -305,6 +359,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = uniform(*tmem_holder);
+  const bool any_far = C::NV && uniform(*far_flag) != 0;
   const int n_tiles = uniform(groups->tiles[a.E]);
   const int nk = (a.k + C::BK - 1) / C::BK;
   const int first_tile = static_cast<int>(blockIdx.x) / CTAS;
@@ -474,9 +529,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int L = first_tile; L < n_tiles; L += grid, ++tile) {
       const QTile t = q_tile<C>(a, *groups, by_m, L);
       const int acc = tile & 1;
-      float alpha = 1.0f;
-      if (a.x_scale != nullptr) alpha = __ldg(a.x_scale);
-      if (a.w_scale != nullptr) alpha *= __ldg(a.w_scale + t.e);
+      const float alpha = C::NV ? lead[t.e] : 1.0f;
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], static_cast<uint32_t>((tile >> 1) & 1)))) {
         if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_EPILOGUE);
         break;
@@ -485,6 +538,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int mrow = t.m0 + 128 * rank + q * 32;  // first output column of this warp
       OutT* out = static_cast<OutT*>(a.out) + static_cast<int64_t>(t.n0) * a.n + mrow;
       const uint32_t tb = tmem_base + (acc ? C::ACC1 : 0u) + (static_cast<uint32_t>(q * 32) << 16);
+      if (C::NV && any_far) {
+        const float shift = tensor_scales(a.x_scale != nullptr ? __ldg(a.x_scale) : 1.0f,
+                                          a.w_scale != nullptr ? __ldg(a.w_scale + t.e) : 1.0f).shift;
+        if (__any_sync(0xffffffffu, shift != 1.0f)) shift_chunks(tb, csel, t.N, shift);
+      }
 #pragma unroll 1
       for (int i = 0; i < C::CHUNKS; ++i) {
         // the two warps of a lane quarter take alternate chunks of 32 rows; the

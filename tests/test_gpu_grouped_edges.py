@@ -76,3 +76,49 @@ def test_a_ragged_group_after_more_than_a_second_of_whole_steps():
         assert ((got - ref).abs() <= tol).all()
     del x, dw
     torch.cuda.empty_cache()
+
+
+# block scales whose sums below are exact: 1 to 4, 2^-9 to 2^-7, 64 to 256 (E4M3)
+BLOCK_SCALES = {"small": [1, 2, 4], "one": [0x38, 0x40, 0x48], "large": [0x68, 0x70, 0x78]}
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("blocks", list(BLOCK_SCALES))
+def test_product_with_tensor_scales_far_from_one(blocks, dt):
+    """The tensor scales' product leaves fp32's range on either side while the results may
+    not. Sums are whole multiples of 21 bits at most, so they are exact, and scales that are
+    powers of two leave one rounding (to a subnormal, or to bf16); the last two pairs add
+    that of their product and that of the sum's product with it, 2^-24 each."""
+    gen = torch.Generator().manual_seed(3)
+    rows, n, k = 80, 72, 800
+    xc = torch.randint(0, 256, (rows, k // 2), generator=gen).to(U8).cuda()
+    wc = torch.randint(0, 256, (2, n, k // 2), generator=gen).to(U8).cuda()
+    xc[[0, 50]] = 0  # sums of zero
+    s = torch.tensor(BLOCK_SCALES[blocks], dtype=U8)
+    xs = s[torch.randint(0, 3, (rows, k // 16), generator=gen)].cuda()
+    wsc = s[torch.randint(0, 3, (2, n, k // 16), generator=gen)].cuda()
+    sums = torch.empty(rows, n, dtype=torch.float64, device="cuda")
+    x, w = torch.empty(rows, k, device="cuda"), torch.empty(2, n, k, device="cuda")
+    M.moe_dequantize_microscaled(NV, xc, xs, None, x)
+    M.moe_dequantize_microscaled(NV, wc, wsc, None, w)
+    off = torch.tensor([0, 33, 80], dtype=torch.int32, device="cuda")
+    sums[:33], sums[33:] = x[:33].double() @ w[0].double().t(), x[33:].double() @ w[1].double().t()
+    sh = M.grouped_shape(rows, 2, n, k, dt)
+    ws = M.grouped_workspace(sh)
+    lo, hi = 2.0 ** -100, 2.0 ** 117
+    pairs = [(2.0 ** 70, 2.0 ** 70, 2.0 ** 58), (2.0 ** -75, 2.0 ** -75, 2.0 ** -58), (lo, lo, 2.0 ** -30), (hi, hi, 1.0),
+             (hi, lo, hi), (lo, hi, lo), (2.0 ** -60, 2.0 ** -68, 2.0 ** -90), (1.0, 2.0 ** -20, 3.0),
+             (1.3 * 2.0 ** -64, 1.7 * 2.0 ** -66, 1.9 * 2.0 ** -70), (1.3 * 2.0 ** 64, 1.7 * 2.0 ** 65, 1.1 * 2.0 ** 66)]
+    for gx, ga, gb in pairs:
+        xg, wg = torch.tensor([gx], device="cuda"), torch.tensor([ga, gb], device="cuda")
+        y = torch.full((rows, n), -77.0, dtype=dt, device="cuda")
+        M.moe_grouped_gemm_microscaled(sh, NV, xc, xs, xg, None, off, wc, wsc, wg, y, ws)
+        assert M.moe_get_device_status(ws) == 0
+        ref = sums * xg.double() * wg.double()[[0] * 33 + [1] * 47].unsqueeze(1)
+        if (gx, ga, gb) in pairs[:-2] and gb != 3.0:
+            assert torch.equal(y, ref.float().to(dt)), (gx, ga, gb)
+        else:
+            fits = ref.abs() < torch.finfo(dt).max
+            tol = (2.0 ** -23 + (2.0 ** -8 if dt == BF else 2.0 ** -24)) * (1 + 2.0 ** -6) * ref.abs() + 2.0 ** -133
+            assert ((y.double() - ref).abs() <= tol)[fits].all(), (gx, ga, gb)
+            assert torch.isinf(y[ref.abs() > 2.0 ** 129]).all()
