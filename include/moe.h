@@ -391,7 +391,8 @@ typedef struct moe_grouped_shape {
 
 size_t moe_grouped_workspace_bytes(void);
 
-/* y[r] = W_e x[r] for every row r of expert e.
+/* y[r] = W_e x[r] for every row r of expert e. The sum of an fp32 result (here and in
+ * moe_grouped_gemm_dgrad) is taken in parts of 512 terms that are added in fp32.
  *   x [device] [rows, k] bf16;  w [device] [n_experts, n, k] bf16
  *   y [device] [rows, n] out_dtype, rows without an owner left as they were
  *   group_start [device] [n_experts + 1] int32 or NULL (the last entry is not read)
@@ -459,6 +460,8 @@ moe_status moe_dequantize_microscaled(int32_t format, int64_t groups, int64_t ro
  *   w_codes [device] [n_experts, n, k / 2], w_scales [device] [n_experts, n, k / 32 or / 16],
  *   w_scale [device] [n_experts] fp32 or NULL for 1 (both NULL for MOE_MXFP4)
  *   the others as for moe_grouped_gemm.
+ * An fp32 result's sum is taken in parts of 8192 terms that are added in fp32, in y:
+ * what y holds is not defined until the call has completed.
  * Tensor scales in [2^-100, 2^117], as the conversions take them: the result is then
  * 0, infinite or subnormal only where the product of the sum and both scales is. */
 moe_status moe_grouped_gemm_microscaled(const moe_grouped_shape* shape, int32_t format, const uint8_t* x_codes,

@@ -65,6 +65,14 @@ struct QCfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SF_BYTES = (1 + BBLK) * SF_BLOCK;  // a slot
   static constexpr bool OVERLAP = BN == 256;
+  // The tensor core's fp32 sum loses up to an ulp a step towards zero (terms of one sign,
+  // against 64 bits: 6e-7 of the result after the 128 steps of k = 8192, 8e-6 after 512).
+  // Where the result is fp32, the accumulator is therefore handed over every SUM_BLOCKS
+  // stages (128 steps) and the parts are added in the result's own place, rounded to
+  // nearest: the registers do not hold a tile's sums beside the rest. (Parts of 32 steps
+  // would make 32768 rows of 4096 in 16 groups 40% slower.)
+  static constexpr bool PARTS = O32;
+  static constexpr int SUM_BLOCKS = 32;
   static constexpr uint32_t ACC1 = OVERLAP ? 192 : BN;  // first column of the second accumulator
   static constexpr uint32_t SFA_COL = 448;
   static constexpr uint32_t SFB_COL = SFA_COL + WORDS * 4;
@@ -220,6 +228,25 @@ __device__ __forceinline__ void shift_chunks(uint32_t tb, int csel, int N, float
     }
   }
   tmem_st_wait();
+}
+
+// r += shift * what store_chunk_turned has left of the parts before at the same place (this
+// thread's own stores).
+__device__ __forceinline__ void add_stored(uint32_t (&r)[32], const float* at, int64_t ld, int rows, int cols,
+                                           float shift, int lane) {
+  const volatile float* p = at + lane;  // (loads in this order, a few in flight: there are no more registers)
+  const int mine = lane < cols ? rows : 0;
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 4) {
+    float had[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      had[j] = j0 + j < mine ? *p : 0.0f;
+      p += ld;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j0 + j] = __float_as_uint(fmaf(had[j], shift, __uint_as_float(r[j0 + j])));
+  }
 }
 
 // Eight words of a scale row from byte `at` on, zero past the row's end. The row starts
@@ -429,26 +456,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint32_t phase = 0;
       int slot = 0;
       uint32_t sf_phase = 0;
-      int tile = 0;
+      int part = 0;  // accumulators handed to the epilogues: one a tile, or one every SUM_BLOCKS stages
       bool ok = true;
-      for (int L = first_tile; L < n_tiles && ok; L += grid, ++tile) {
-        const int acc = tile & 1;
-        // the accumulator is free: with shared columns once the tile before has let
-        // go of them (its epilogue is then past the tile before that)
-        bool free = true;
-        if constexpr (C::OVERLAP) {
-          if (tile > 0) free = mbar_wait(&acc_empty[0], static_cast<uint32_t>((tile - 1) & 1));
-        } else {
-          free = mbar_wait(&acc_empty[acc], static_cast<uint32_t>(((tile >> 1) & 1) ^ 1));
-        }
-        if (!__all_sync(0xffffffffu, free)) {
-          if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_MMA);
-          break;
-        }
-        const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
+      for (int L = first_tile; L < n_tiles && ok; L += grid) {
         const uint32_t n_bits = uniform(static_cast<uint32_t>(q_tile<C>(a, *groups, by_m, L).N) >> 3 << 17);
         for (int kb = 0; kb < nk; ++kb) {
           const int sub = kb % C::SF_STAGES_PER;
+          const int acc = part & 1;
+          const bool first = kb == 0 || (C::PARTS && kb % C::SUM_BLOCKS == 0);
+          if (first) {
+            // the accumulator is free: with shared columns once the part before has let
+            // go of them (its epilogue is then past the part before that)
+            bool free = true;
+            if constexpr (C::OVERLAP) {
+              if (part > 0) free = mbar_wait(&acc_empty[0], static_cast<uint32_t>((part - 1) & 1));
+            } else {
+              free = mbar_wait(&acc_empty[acc], static_cast<uint32_t>(((part >> 1) & 1) ^ 1));
+            }
+            if (!__all_sync(0xffffffffu, free)) {
+              if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_MMA);
+              ok = false;
+              break;
+            }
+          }
           if (!__all_sync(0xffffffffu,
                           (sub != 0 || mbar_wait(&sf_full[slot], sf_phase)) && mbar_wait(&full[stage], phase))) {
             if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_MMA);
@@ -457,7 +487,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           tc_fence_after();
           const bool slot_done = sub == C::SF_STAGES_PER - 1 || kb + 1 == nk;
+          const bool part_done = kb + 1 == nk || (C::PARTS && (kb + 1) % C::SUM_BLOCKS == 0);
           if (elect_one()) {
+            const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
             const uint32_t off = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
             const uint32_t sfa =
                 (sf_lo + static_cast<uint32_t>(slot) * (C::SF_BYTES >> 4) + sub * (C::WORDS * 512 >> 4)) & 0x3FFFu;
@@ -480,17 +512,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 constexpr uint32_t odd = micro_idesc(C::NV, C::BM, 0, 2);
                 umma_micro<C::NV, C::PAIR>(d_tmem, desc0.a + off + kk * 2, desc0.b + off + kk * 2,
                                            (C::NV || (kk & 1) == 0 ? even : odd) | n_bits, tmem_base + C::SFA_COL + w * 4,
-                                           tmem_base + C::SFB_COL + w * C::BBLK * 4, (kb > 0 || kk > 0) ? 1u : 0u);
+                                           tmem_base + C::SFB_COL + w * C::BBLK * 4, (first && kk == 0) ? 0u : 1u);
               }
             }
             if constexpr (C::PAIR) {
               umma_commit_pair(&empty[stage], 0x3);
               if (slot_done) umma_commit_pair(&sf_empty[slot], 0x3);
+              if (part_done) umma_commit_pair(&acc_full[acc], 0x3);
             } else {
               umma_commit(&empty[stage]);
               if (slot_done) umma_commit(&sf_empty[slot]);
+              if (part_done) umma_commit(&acc_full[acc]);
             }
           }
+          if (part_done) ++part;
           if (slot_done && ++slot == C::SF_SLOTS) {
             slot = 0;
             sf_phase ^= 1u;
@@ -499,13 +534,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             stage = 0;
             phase ^= 1u;
           }
-        }
-        if (!ok) break;
-        if (elect_one()) {
-          if constexpr (C::PAIR)
-            umma_commit_pair(&acc_full[acc], 0x3);
-          else
-            umma_commit(&acc_full[acc]);
         }
       }
       if (elect_one()) {
@@ -516,7 +544,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!mbar_wait(drain, 0)) report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
         // a pair's epilogues have released every accumulator, so that no remote arrival
         // reaches this CTA after it has ended
-        if (C::PAIR && tile > 0 && !mbar_wait(&acc_empty[0], static_cast<uint32_t>((tile - 1) & 1)))
+        if (C::PAIR && part > 0 && !mbar_wait(&acc_empty[0], static_cast<uint32_t>((part - 1) & 1)))
           report(a.status, DEV_WAIT_TIMEOUT_DRAIN);
       }
     }
@@ -525,51 +553,66 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     using OutT = typename C::OutT;
     const int q = warp & 3;
     const int csel = (warp - 2) >> 2;
-    int tile = 0;
-    for (int L = first_tile; L < n_tiles; L += grid, ++tile) {
+    const int parts = C::PARTS ? (nk + C::SUM_BLOCKS - 1) / C::SUM_BLOCKS : 1;
+    int part = 0;
+    bool ok = true;
+    for (int L = first_tile; L < n_tiles && ok; L += grid) {
       const QTile t = q_tile<C>(a, *groups, by_m, L);
-      const int acc = tile & 1;
       const float alpha = C::NV ? lead[t.e] : 1.0f;
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], static_cast<uint32_t>((tile >> 1) & 1)))) {
-        if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_EPILOGUE);
-        break;
-      }
-      tc_fence_after();
-      const int mrow = t.m0 + 128 * rank + q * 32;  // first output column of this warp
-      OutT* out = static_cast<OutT*>(a.out) + static_cast<int64_t>(t.n0) * a.n + mrow;
-      const uint32_t tb = tmem_base + (acc ? C::ACC1 : 0u) + (static_cast<uint32_t>(q * 32) << 16);
-      if (C::NV && any_far) {
-        const float shift = tensor_scales(a.x_scale != nullptr ? __ldg(a.x_scale) : 1.0f,
-                                          a.w_scale != nullptr ? __ldg(a.w_scale + t.e) : 1.0f).shift;
-        if (__any_sync(0xffffffffu, shift != 1.0f)) shift_chunks(tb, csel, t.N, shift);
-      }
+      for (int p = 0; p < parts; ++p, ++part) {
+        const int acc = part & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], static_cast<uint32_t>((part >> 1) & 1)))) {
+          if (lane == 0) report(a.status, DEV_WAIT_TIMEOUT_EPILOGUE);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool last = p + 1 == parts;
+        const int mrow = t.m0 + 128 * rank + q * 32;  // first output column of this warp
+        OutT* out = static_cast<OutT*>(a.out) + static_cast<int64_t>(t.n0) * a.n + mrow;
+        const uint32_t tb = tmem_base + (acc ? C::ACC1 : 0u) + (static_cast<uint32_t>(q * 32) << 16);
+        float shift = 1.0f;
+        if (C::NV && any_far && last) {
+          shift = tensor_scales(a.x_scale != nullptr ? __ldg(a.x_scale) : 1.0f,
+                                a.w_scale != nullptr ? __ldg(a.w_scale + t.e) : 1.0f).shift;
+          if (__any_sync(0xffffffffu, shift != 1.0f)) shift_chunks(tb, csel, t.N, shift);
+        }
 #pragma unroll 1
-      for (int i = 0; i < C::CHUNKS; ++i) {
-        // the two warps of a lane quarter take alternate chunks of 32 rows; the
-        // accumulator columns shared with the other accumulator come first: the upper
-        // end of the first accumulator, the lower end of the second
-        const int j = C::OVERLAP && acc == 0 ? C::CHUNKS - 1 - i : i;
-        const int c = (2 * j + csel) * 32;
-        uint32_t r[32];
-        if (c < t.N) {
-          tmem_ld32(tb + c, r);
-          tmem_ld_wait();
-        }
-        if (i == (C::OVERLAP ? 0 : C::CHUNKS - 1)) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (C::PAIR)
-              mbar_arrive_cluster_relaxed(acc_empty_leader);
-            else
-              mbar_arrive_relaxed(&acc_empty[C::OVERLAP ? 0 : acc]);
+        for (int i = 0; i < C::CHUNKS; ++i) {
+          // the two warps of a lane quarter take alternate chunks of 32 rows; the
+          // accumulator columns shared with the other accumulator come first: the upper
+          // end of the first accumulator, the lower end of the second
+          const int j = C::OVERLAP && acc == 0 ? C::CHUNKS - 1 - i : i;
+          const int c = (2 * j + csel) * 32;
+          uint32_t r[32];
+          if (c < t.N) {
+            tmem_ld32(tb + c, r);
+            tmem_ld_wait();
           }
-        }
-        if (c < t.N) {
-          float v[32];
+          if (i == (C::OVERLAP ? 0 : C::CHUNKS - 1)) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (C::PAIR)
+                mbar_arrive_cluster_relaxed(acc_empty_leader);
+              else
+                mbar_arrive_relaxed(&acc_empty[C::OVERLAP ? 0 : acc]);
+            }
+          }
+          if (c < t.N) {
+            float v[32];
+            OutT* at = out + static_cast<int64_t>(c) * a.n;
+            int ld = a.n;
+            if constexpr (C::PARTS) {
+              // (opaque: the rows' addresses are not kept from part to part, in registers that there are not)
+              asm volatile("" : "+l"(at), "+r"(ld));
+              if (p > 0) add_stored(r, at, ld, t.left - c, a.n - mrow, shift, lane);
+            }
+            const float by = last ? alpha : 1.0f;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]) * alpha;
-          store_chunk_turned<OutT>(v, out + static_cast<int64_t>(c) * a.n, a.n, t.left - c, a.n - mrow, lane);
+            for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]) * by;
+            store_chunk_turned<OutT>(v, at, ld, t.left - c, a.n - mrow, lane);
+          }
         }
       }
     }

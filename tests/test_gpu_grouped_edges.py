@@ -122,3 +122,85 @@ def test_product_with_tensor_scales_far_from_one(blocks, dt):
             tol = (2.0 ** -23 + (2.0 ** -8 if dt == BF else 2.0 ** -24)) * (1 + 2.0 ** -6) * ref.abs() + 2.0 ** -133
             assert ((y.double() - ref).abs() <= tol)[fits].all(), (gx, ga, gb)
             assert torch.isinf(y[ref.abs() > 2.0 ** 129]).all()
+
+
+# fp32 results of long sums: the tensor core may lose up to an ulp of the running sum a step
+# towards zero, over many elements half of one on average; with terms of one sign the sum
+# grows evenly, so a part of s steps loses at most s/4 2^-23 of itself in the norm. The parts
+# are added to nearest, half an ulp of at most the whole each.
+def long_sum_bound(steps, parts):
+    return steps / 4 * 2.0 ** -23 + parts * 2.0 ** -24
+
+
+def relative(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("counts,n", [([3], 64), ([40, 70], 256), ([700, 300], 2048)], ids=["few", "rows", "pairs"])
+@pytest.mark.parametrize("k", [32768, 16416, 6176])
+def test_product_of_long_sums_in_fp32(fmt, counts, n, k):
+    """Parts of 8192 terms (128 steps), on every layout of a tile; 16416 ends inside a part."""
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    total, E, b = sum(counts), len(counts), 16 if fmt == NV else 32
+
+    def operand(*shape):
+        v = torch.rand(*shape, generator=gen, device="cuda") + 0.1
+        v *= torch.exp2(torch.randint(-6, 7, (*shape[:-1], 1), generator=gen, device="cuda").float())
+        codes = torch.empty(*shape[:-1], k // 2, dtype=U8, device="cuda")
+        scales = torch.empty(*shape[:-1], k // b, dtype=U8, device="cuda")
+        M.moe_quantize_microscaled(fmt, v, None, codes, scales)
+        M.moe_dequantize_microscaled(fmt, codes, scales, None, v)
+        return codes, scales, v.double()
+
+    xc, xs, x = operand(total, k)
+    wc, wsc, w = operand(E, n, k)
+    ends = torch.tensor([0] + counts).cumsum(0)
+    sh = M.grouped_shape(total, E, n, k, F32)
+    ws = M.grouped_workspace(sh)
+    cases = [(xs, x, wsc, w, 1.0, 1.0)]
+    if fmt == NV:
+        cases.append((xs, x, wsc, w, 0.75, 0.6))
+        # block scales of 2^-9 on both sides and tensor scales whose product is no fp32 number
+        xs1, ws1, x1, w1 = torch.ones_like(xs), torch.ones_like(wsc), x.float(), w.float()
+        M.moe_dequantize_microscaled(NV, xc, xs1, None, x1)
+        M.moe_dequantize_microscaled(NV, wc, ws1, None, w1)
+        cases.append((xs1, x1.double(), ws1, w1.double(), 2.0 ** 66, 2.0 ** 63))
+    off = ends.int().cuda()
+    for xs, x, wsc, w, gx, gw in cases:
+        xg, wg = torch.tensor([gx], device="cuda"), torch.full((E,), gw, device="cuda")
+        y = torch.full((total, n), -77.0, device="cuda")
+        M.moe_grouped_gemm_microscaled(sh, fmt, xc, xs, xg if fmt == NV else None, None, off, wc, wsc,
+                                       wg if fmt == NV else None, y, ws)
+        assert M.moe_get_device_status(ws) == 0
+        for e in range(E):
+            lo, hi = int(ends[e]), int(ends[e + 1])
+            ref = x[lo:hi] @ w[e].t() * (xg.double() * wg[e].double())
+            got = y[lo:hi]
+            # sums of up to 32768 36 2^-18 times 2^129 pass fp32's largest number: those are infinite
+            above = ref > torch.finfo(F32).max * (1 + 2.0 ** -18)
+            assert torch.isinf(got[above]).all()
+            below = ref < torch.finfo(F32).max * (1 - 2.0 ** -18)
+            if below.any():  # (and 2^-24 each for the tensor scales' product and for the sum's with it)
+                assert relative(got[below], ref[below]) <= long_sum_bound(128, -(-k // 8192)) + 2.0 ** -23
+
+
+def test_products_of_long_sums_in_fp32():
+    """The 16-bit products: parts of 512 terms (32 steps), over the width and over the rows."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    positive = lambda *s: (torch.rand(*s, generator=gen, device="cuda") + 0.1).to(BF)  # noqa: E731
+    for rows, n, k in ((130, 264, 8192), (130, 8192, 264), (8200, 264, 256), (8200, 1024, 1024)):
+        x, dy, w = positive(rows, k), positive(rows, n), positive(1, n, k)
+        off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        sh = M.grouped_shape(rows, 1, n, k, F32)
+        ws = M.grouped_workspace(sh)
+        y, dx = torch.empty(rows, n, device="cuda"), torch.empty(rows, k, device="cuda")
+        dw = torch.empty(1, n, k, device="cuda")
+        M.moe_grouped_gemm(sh, x, None, off, w, y, ws)
+        M.moe_grouped_gemm_dgrad(sh, dy, None, off, w, dx, ws)
+        M.moe_grouped_gemm_wgrad(sh, dy, x, None, off, dw, ws)
+        assert M.moe_get_device_status(ws) == 0
+        xd, dyd, wd = x.double(), dy.double(), w[0].double()
+        assert relative(y, xd @ wd.t()) <= long_sum_bound(32, -(-k // 512))
+        assert relative(dx, dyd @ wd) <= long_sum_bound(32, -(-n // 512))
+        assert relative(dw[0], dyd.t() @ xd) <= long_sum_bound(32, -(-rows // 512))
