@@ -428,7 +428,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy
  * holds an infinity or a NaN gets the NaN scale and reads back as NaN, and so does
  * every block under a tensor scale outside [2^-100, 2^117].
  * Matrices are [groups, rows, cols] with one tensor scale per group (an expert's
- * weight, or all rows of an activation buffer): groups >= 1, rows >= 0, cols a
+ * weight, or an activation buffer): groups >= 1, rows >= 0, cols a
  * multiple of 32 in [32, 2^20], at most 2^40 elements. All pointers but the tensor
  * scale's are 16-byte aligned. */
 typedef enum moe_microscaled_format { MOE_MXFP4 = 0, MOE_NVFP4 = 1 } moe_microscaled_format;
@@ -438,6 +438,18 @@ typedef enum moe_microscaled_format { MOE_MXFP4 = 0, MOE_NVFP4 = 1 } moe_microsc
  *   x [device] [groups, rows, cols] of `dtype` (moe_dtype);  scale [device] [groups] fp32 out */
 moe_status moe_tensor_scale_microscaled(int64_t groups, int64_t rows, int64_t cols, int32_t dtype, const void* x,
                                         float* scale, cudaStream_t stream);
+
+/* The same over the rows of one buffer that some expert owns: the scale of an activation
+ * buffer in groups. Rows without an owner are not read. (moe_tensor_scale_microscaled, and
+ * the conversions, take every row of a matrix, and moe_dispatch leaves the rows behind the
+ * last group's as they were: a large number there would give a g under which the real rows
+ * round to zero. The codes that quantisation gives such rows are used by no product.)
+ *   shape [host] the product's: rows, n_experts and k (a multiple of 32)
+ *   x [device] [rows, k] of `dtype`;  scale [device] [1] fp32 out
+ *   group_start, offsets, ws as for the ragged products */
+moe_status moe_grouped_tensor_scale_microscaled(const moe_grouped_shape* shape, int32_t dtype, const void* x,
+                                                const int32_t* group_start, const int32_t* offsets, float* scale,
+                                                void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*   x            [device] [groups, rows, cols] of `dtype`
  *   tensor_scale [device] [groups] fp32, or NULL for 1 (must be NULL for MOE_MXFP4)

@@ -45,8 +45,9 @@ EXPORTS = (
     "moe_forward_decode", "moe_forward_host", "moe_forward_host_async", "moe_backward", "moe_rmsnorm", "moe_combine_residual",
     "moe_stack_forward", "moe_stack_forward_trace", "moe_expert_choice_capacity", "moe_route_expert_choice",
     "moe_forward_expert_choice", "moe_grouped_workspace_bytes", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
-    "moe_grouped_gemm_wgrad", "moe_tensor_scale_microscaled", "moe_quantize_microscaled",
-    "moe_dequantize_microscaled", "moe_grouped_gemm_microscaled", "moe_set_stage_events", "moe_get_device_status",
+    "moe_grouped_gemm_wgrad", "moe_tensor_scale_microscaled", "moe_grouped_tensor_scale_microscaled",
+    "moe_quantize_microscaled", "moe_dequantize_microscaled", "moe_grouped_gemm_microscaled", "moe_set_stage_events",
+    "moe_get_device_status",
 )
 STAGE_EVENTS = 6
 STAGES = ("router", "dispatch", "gate_up", "down", "combine")
@@ -125,6 +126,7 @@ _SIGS = {
     "moe_grouped_gemm_dgrad": (ctypes.c_int, [_GSH, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_grouped_gemm_wgrad": (ctypes.c_int, [_GSH, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_tensor_scale_microscaled": (ctypes.c_int, [_I64, _I64, _I64, _I32, _P, _P, _P]),
+    "moe_grouped_tensor_scale_microscaled": (ctypes.c_int, [_GSH, _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_quantize_microscaled": (ctypes.c_int, [_I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P]),
     "moe_dequantize_microscaled": (ctypes.c_int, [_I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P]),
     "moe_grouped_gemm_microscaled": (ctypes.c_int, [_GSH, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
@@ -647,12 +649,26 @@ def _micro_args(fmt, t, name, tensor_scale, codes, scales, dev):
 
 def moe_tensor_scale_microscaled(x, scale, stream=None):
     """scale[g] = max(amax of x[g] / 2688, 2^-100), the tensor scale MOE_NVFP4 blocks are
-    scaled against. x: [groups, rows, cols], or [rows, cols] as one group."""
+    scaled against. x: [groups, rows, cols], or [rows, cols] as one group. Every row counts;
+    for a buffer of experts' rows see moe_grouped_tensor_scale_microscaled."""
     dev = _current_device()
     G, R, K, dt = _micro_shape(x, "x")
     st = lib().moe_tensor_scale_microscaled(G, R, K, dt, _arg(x, x.dtype, x.shape, "x", dev),
                                             _arg(scale, torch.float32, (G,), "scale", dev), _raw_stream(stream, dev))
     _check(st, "moe_tensor_scale_microscaled")
+
+
+def moe_grouped_tensor_scale_microscaled(shape, x, group_start, offsets, scale, ws, stream=None):
+    """moe_tensor_scale_microscaled of x [rows, k] over the rows that some expert owns, scale
+    [1]: rows of the buffer without an owner may hold anything."""
+    dev = _current_device()
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_CODE:
+        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
+    gs, off = _group_args(shape, group_start, offsets, dev)
+    st = lib().moe_grouped_tensor_scale_microscaled(
+        ctypes.byref(shape), _DTYPE_CODE[x.dtype], _arg(x, x.dtype, (shape.rows, shape.k), "x", dev), gs, off,
+        _arg(scale, torch.float32, (1,), "scale", dev), _workspace_arg(ws, dev), ws.numel(), _raw_stream(stream, dev))
+    _check(st, "moe_grouped_tensor_scale_microscaled")
 
 
 def moe_quantize_microscaled(fmt, x, tensor_scale, codes, scales, stream=None):

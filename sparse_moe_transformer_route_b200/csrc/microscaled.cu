@@ -22,8 +22,7 @@
 // tensors take one piece a thread, which reaches four times as many SMs. A block's
 // threads (1 to 4) find amax with shuffles. Quantisation goes from the end of a group to
 // its start: what the tensor scale's pass has just read is still in L2 there.
-#include "moe_internal.h"
-#include "sm100.cuh"
+#include "ragged.cuh"
 
 namespace moe {
 namespace {
@@ -339,11 +338,57 @@ __global__ void __launch_bounds__(kThreads)
 // integer atomic maximum (whose order does not matter) over a zeroed array.
 constexpr int kMaxCluster = 8;
 
+constexpr int kTurnPieces = 4 * kThreads;  // of a CTA at a time
+
+// The largest finite magnitude (as an integer) of a thread's four pieces p0, p0 + kThreads,
+// ... of the `pieces` at `src`.
+template <typename T>
+__device__ __forceinline__ uint32_t top_of_turn(const T* src, int64_t p0, int64_t pieces, bool wide) {
+  constexpr int EPT = elems_per_thread<T>();
+  constexpr int U = kTurnPieces / kThreads;
+  uint32_t raw[U][8];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int64_t p = p0 + j * kThreads;
+    if (p < pieces) {
+      if (wide)
+        load32(src + p * EPT, raw[j]);
+      else
+        load16x2(src + p * EPT, raw[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[j][i] = 0u;
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    float v[EPT];
+    widen<T>(raw[j], v);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+      top = max(top, m < 0x7F800000u ? m : 0u);
+    }
+  }
+  return top;
+}
+
+// The scale's bits of the CTA's largest magnitude, in thread 0; ends behind a block barrier.
+__device__ __forceinline__ uint32_t cta_scale(uint32_t top, uint32_t (&warp_top)[kThreads / 32]) {
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return 0;
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) top = max(top, warp_top[i]);
+  return __float_as_uint(fmaxf(__uint_as_float(top) / 2688.0f, kMinTensorScale));
+}
+
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads)
     tensor_scale_kernel(const T* __restrict__ x, float* __restrict__ scale, int64_t groups, int64_t pieces_per_group) {
   constexpr int EPT = elems_per_thread<T>();
-  constexpr int U = 4;
   __shared__ uint32_t warp_top[kThreads / 32];
   __shared__ uint32_t cta_top[kMaxCluster];
   pdl_trigger();
@@ -356,42 +401,10 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t grp = blockIdx.y; grp < groups; grp += gridDim.y) {
     const T* src = x + grp * pieces_per_group * EPT;
     uint32_t top = 0;
-    for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * (U * kThreads) + threadIdx.x; p0 < pieces_per_group;
-         p0 += static_cast<int64_t>(gridDim.x) * (U * kThreads)) {
-      uint32_t raw[U][8];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int64_t p = p0 + j * kThreads;
-        if (p < pieces_per_group) {
-          if (wide)
-            load32(src + p * EPT, raw[j]);
-          else
-            load16x2(src + p * EPT, raw[j]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) raw[j][i] = 0u;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        float v[EPT];
-        widen<T>(raw[j], v);
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-          top = max(top, m < 0x7F800000u ? m : 0u);
-        }
-      }
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
-    __syncthreads();
-    uint32_t mine = 0;
-    if (threadIdx.x == 0) {
-#pragma unroll
-      for (int i = 1; i < kThreads / 32; ++i) top = max(top, warp_top[i]);
-      mine = __float_as_uint(fmaxf(__uint_as_float(top) / 2688.0f, kMinTensorScale));
-    }
+    for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * kTurnPieces + threadIdx.x; p0 < pieces_per_group;
+         p0 += static_cast<int64_t>(gridDim.x) * kTurnPieces)
+      top = max(top, top_of_turn(src, p0, pieces_per_group, wide));
+    uint32_t mine = cta_scale(top, warp_top);
     if constexpr (CLUSTER) {
       if (grp == blockIdx.y) {  // the first of this cluster's groups
         __syncwarp();
@@ -417,6 +430,59 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
   }
+}
+
+// One scale over the rows that some expert owns: group e is pieces_per_row * count_e pieces in
+// a row, and the groups' turns are dealt to the CTAs one after the other. The rows between
+// and behind the groups hold whatever the buffer held before (moe_dispatch zeroes the pads
+// of a group, and leaves the rows behind the last one) and are not read. A thread works
+// out one group, and a turn finds its group in the sums (walking over 64 groups in every
+// warp took 25 us).
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    tensor_scale_owned_kernel(const T* __restrict__ x, const int32_t* __restrict__ group_start,
+                              const int32_t* __restrict__ offsets, int E, int64_t rows, int pieces_per_row,
+                              float* __restrict__ scale, int32_t* status) {
+  constexpr int EPT = elems_per_thread<T>();
+  static_assert(kThreads >= kMaxExperts, "a thread a group");
+  __shared__ uint32_t warp_top[kThreads / 32];
+  __shared__ int32_t start[kMaxExperts], count[kMaxExperts];
+  __shared__ int64_t first[kThreads], warp_sum[kThreads / 32];  // number of a group's first turn
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  pdl_trigger();
+  pdl_wait();
+  int64_t turns = 0;
+  if (static_cast<int>(threadIdx.x) < E) {
+    const int e = static_cast<int>(threadIdx.x);
+    checked_group(group_start, offsets, e, rows, &start[e], &count[e], status);
+    turns = (static_cast<int64_t>(count[e]) * pieces_per_row + kTurnPieces - 1) / kTurnPieces;
+  }
+  int64_t upto = turns;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) first[threadIdx.x] = total + upto - turns;
+    total += warp_sum[w];
+  }
+  __syncthreads();
+  const bool wide = aligned32(x);
+  uint32_t top = 0;
+  for (int64_t turn = blockIdx.x; turn < total; turn += gridDim.x) {
+    int e = -1;  // the last group that starts at this turn or before (those without rows start with the next)
+    for (int base = 0; base < E; base += 32)
+      e += __popc(__ballot_sync(0xffffffffu, base + lane < E && first[base + lane] <= turn));
+    top = max(top, top_of_turn(x + static_cast<int64_t>(start[e]) * pieces_per_row * EPT,
+                               (turn - first[e]) * kTurnPieces + threadIdx.x,
+                               static_cast<int64_t>(count[e]) * pieces_per_row, wide));
+  }
+  const uint32_t mine = cta_scale(top, warp_top);
+  if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(scale), mine);
 }
 
 // A CTA for every per_turn pieces of a group, a group each in y.
@@ -455,7 +521,26 @@ cudaError_t run_tensor_scale(int64_t groups, int64_t pieces, const void* x, floa
                           pieces);
 }
 
+template <typename T>
+cudaError_t run_tensor_scale_owned(int64_t rows, int E, int k, const void* x, const int32_t* gs, const int32_t* off,
+                                   float* scale, int32_t* status, cudaStream_t st) {
+  const int pieces_per_row = k / elems_per_thread<T>();
+  const int64_t turns = (rows * pieces_per_row + kTurnPieces - 1) / kTurnPieces + E;  // at most
+  const int64_t most = 4 * static_cast<int64_t>(device_sm_count());
+  const cudaError_t e = cudaMemsetAsync(scale, 0, 4, st);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(tensor_scale_owned_kernel<T>, dim3(static_cast<unsigned>(turns < most ? turns : most)),
+                          dim3(kThreads), 0, st, nullptr, 0, static_cast<const T*>(x), gs, off, E, rows, pieces_per_row,
+                          scale, status);
+}
+
 }  // namespace
+
+cudaError_t launch_tensor_scale_owned(int64_t rows, int E, int k, bool fp32, const void* x, const int32_t* gs,
+                                      const int32_t* off, float* scale, int32_t* status, cudaStream_t st) {
+  return fp32 ? run_tensor_scale_owned<float>(rows, E, k, x, gs, off, scale, status, st)
+              : run_tensor_scale_owned<__nv_bfloat16>(rows, E, k, x, gs, off, scale, status, st);
+}
 
 cudaError_t launch_tensor_scale(int64_t groups, int64_t per_group, bool fp32, const void* x, float* scale,
                                 cudaStream_t st) {

@@ -345,6 +345,18 @@ moe_status moe_tensor_scale_microscaled(int64_t groups, int64_t rows, int64_t co
   return MOE_OK;
 }
 
+moe_status moe_grouped_tensor_scale_microscaled(const moe_grouped_shape* shape, int32_t dtype, const void* x,
+                                                const int32_t* group_start, const int32_t* offsets, float* scale,
+                                                void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const moe_status r = grouped_prepare(shape, 32, offsets, ws, ws_bytes);
+  if (r != MOE_OK) return r;
+  if ((dtype != MOE_BF16 && dtype != MOE_FP32) || !usable(x, shape->rows) || scale == nullptr) return MOE_ERR_INVALID_ARG;
+  if (device_ready() != MOE_OK) return MOE_ERR_NO_DEVICE;
+  MOE_TRY(launch_tensor_scale_owned(shape->rows, shape->n_experts, shape->k, dtype == MOE_FP32, x, group_start, offsets,
+                                    scale, at<int32_t>(ws, 0), stream));
+  return MOE_OK;
+}
+
 moe_status moe_quantize_microscaled(int32_t format, int64_t groups, int64_t rows, int64_t cols, int32_t dtype,
                                     const void* x, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
                                     cudaStream_t stream) {

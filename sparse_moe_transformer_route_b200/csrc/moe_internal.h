@@ -221,6 +221,9 @@ cudaError_t launch_ragged_microscaled(bool nv, int64_t rows, int E, int n, int k
 // Microscaled 4-bit values (microscaled.cu). per_group: elements of a group.
 cudaError_t launch_tensor_scale(int64_t groups, int64_t per_group, bool fp32, const void* x, float* scale,
                                 cudaStream_t st);
+// One scale over the rows of a buffer [rows, k] that E groups own.
+cudaError_t launch_tensor_scale_owned(int64_t rows, int E, int k, bool fp32, const void* x, const int32_t* gs,
+                                      const int32_t* off, float* scale, int32_t* status, cudaStream_t st);
 cudaError_t launch_quantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const void* x,
                             const float* tensor_scale, uint8_t* codes, uint8_t* scales, cudaStream_t st);
 cudaError_t launch_dequantize(bool nv, int64_t groups, int64_t per_group, bool fp32, const uint8_t* codes,

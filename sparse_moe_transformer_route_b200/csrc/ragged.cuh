@@ -44,24 +44,29 @@ __device__ __forceinline__ int rows_a_tile(int count) {
   return min(MOST, max(UNIT, ((count + least - 1) / least + UNIT - 1) / UNIT * UNIT));
 }
 
-// Reads the layout (all threads of the CTA; it ends with a block barrier). A group
-// that does not lie inside [0, rows) is recorded and treated as empty, so that no
-// later access depends on a bad offset. cols: column tiles of a row tile. SORTED: the
+// The rows of group e. A group that does not lie inside [0, rows) is recorded and treated
+// as empty, so that no later access depends on a bad offset.
+__device__ __forceinline__ void checked_group(const int32_t* group_start, const int32_t* offsets, int e, int64_t rows,
+                                              int32_t* start, int32_t* count, int32_t* status) {
+  const int64_t lo = offsets[e], hi = offsets[e + 1];
+  const int64_t s = group_start != nullptr ? group_start[e] : lo;
+  int64_t c = hi - lo;
+  if (c < 0 || (c > 0 && (s < 0 || s + c > rows))) {  // (an empty group may start anywhere)
+    report(status, DEV_BAD_GROUP);
+    c = 0;
+  }
+  *start = c > 0 ? static_cast<int32_t>(s) : 0;
+  *count = static_cast<int32_t>(c);
+}
+
+// Reads the layout (all threads of the CTA; it ends with a block barrier). cols: column tiles of a row tile. SORTED: the
 // experts come by falling row count (equal counts in order of e).
 template <int MOST, int UNIT, bool SORTED>
 __device__ __forceinline__ void load_groups(RaggedGroups* g, const int32_t* group_start, const int32_t* offsets, int E,
                                             int64_t rows, int cols, int32_t* status) {
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    const int64_t lo = offsets[e], hi = offsets[e + 1];
-    const int64_t s = group_start != nullptr ? group_start[e] : lo;
-    int64_t c = hi - lo;
-    if (c < 0 || (c > 0 && (s < 0 || s + c > rows))) {  // (an empty group may start anywhere)
-      report(status, DEV_BAD_GROUP);
-      c = 0;
-    }
-    g->start[e] = c > 0 ? static_cast<int32_t>(s) : 0;
-    g->count[e] = static_cast<int32_t>(c);
-    g->per[e] = rows_a_tile<MOST, UNIT>(static_cast<int>(c));
+    checked_group(group_start, offsets, e, rows, &g->start[e], &g->count[e], status);
+    g->per[e] = rows_a_tile<MOST, UNIT>(g->count[e]);
     if constexpr (!SORTED) g->order[e] = e;
   }
   __syncthreads();

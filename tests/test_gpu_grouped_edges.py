@@ -204,3 +204,96 @@ def test_products_of_long_sums_in_fp32():
         assert relative(y, xd @ wd.t()) <= long_sum_bound(32, -(-k // 512))
         assert relative(dx, dyd @ wd) <= long_sum_bound(32, -(-n // 512))
         assert relative(dw[0], dyd.t() @ xd) <= long_sum_bound(32, -(-rows // 512))
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("how", ["packed", "padded", "gaps", "slack"])
+@pytest.mark.parametrize("counts,k", [([1], 32), ([0, 1, 127, 128, 129, 300, 0, 5], 96), ([40] * 64, 2048), ([0, 0], 64),
+                                      ([3000, 1, 0, 77], 1056), ([2] * 256, 512)], ids=lambda c: str(c)[:12])
+def test_tensor_scale_of_owned_rows(counts, k, how, dt):
+    """Bit for bit; rows without an owner hold large numbers and NaN."""
+    from tests.test_gpu_ragged import layout
+    gs, off, starts, total = layout(counts, how)
+    x = torch.full((total, k), 1e30, dtype=dt, device="cuda")
+    x[::2] = float("nan")
+    amax = torch.zeros(1, device="cuda")
+    for i, (s, c) in enumerate(zip(starts, counts)):
+        rows = torch.randn(c, k, device="cuda") * 2.0 ** (i % 5)
+        if c > 3:
+            rows[1, 0], rows[2, k - 1] = float("inf"), float("nan")
+        x[s:s + c] = rows.to(dt)
+        finite = torch.where(torch.isfinite(x[s:s + c]), x[s:s + c], torch.zeros_like(x[s:s + c]))
+        if c:
+            amax = torch.maximum(amax, finite.float().abs().max())
+    sh = M.grouped_shape(total, len(counts), 8, k)
+    ws = M.grouped_workspace(sh)
+    g = torch.full((1,), -5.0, device="cuda")
+    for _ in range(2):
+        M.moe_grouped_tensor_scale_microscaled(sh, x, gs, off, g, ws)
+        assert M.moe_get_device_status(ws) == 0
+        assert torch.equal(g, tensor_scale(amax))
+
+
+def test_tensor_scale_of_owned_rows_without_rows_and_with_bad_groups():
+    sh, ws = M.grouped_shape(0, 2, 8, 64), M.grouped_workspace()
+    g = torch.full((1,), -5.0, device="cuda")
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    M.moe_grouped_tensor_scale_microscaled(sh, torch.empty(0, 64, device="cuda"), None, none, g, ws)
+    assert M.moe_get_device_status(ws) == 0 and g.item() == 2.0 ** -100
+    sh = M.grouped_shape(10, 2, 8, 64)
+    x = torch.ones(10, 64, device="cuda")
+    x[4:] = 9.0
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for gs, off in ((None, i32(0, 4, 11)), (i32(0, -1, 0), i32(0, 4, 6)), (i32(0, 9, 0), i32(0, 4, 6)), (None, i32(0, 4, 2))):
+        M.moe_grouped_tensor_scale_microscaled(sh, x, gs, off, g, ws)
+        assert M.moe_get_device_status(ws) == 0x203
+        assert torch.equal(g, tensor_scale(torch.ones(1, device="cuda")))
+
+
+def test_quantised_product_on_a_buffer_with_leftovers():
+    """moe_dispatch leaves the rows behind the last group as they were. Whatever an earlier
+    step, or nobody, left there: the same tokens give the same product, bit for bit, in a
+    call captured once."""
+    T, E, top, d, f = 24, 8, 2, 256, 320
+    gen = torch.Generator().manual_seed(9)
+    cfg = M.config(T, d, E, top, 128)
+    P = M.moe_padded_rows(cfg)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    off, gs, perm, inv = i32(E + 1), i32(E + 1), i32(T * top), i32(T * top)
+    idx = torch.stack([torch.randperm(E, generator=gen)[:top] for _ in range(T)]).to(torch.int32).cuda()
+    x = torch.randn(T, d, generator=gen).to(BF).cuda()
+    xp = torch.zeros(P, d, dtype=BF, device="cuda")
+    w = (torch.randn(E, f, d, generator=gen) * 0.02).to(BF).cuda()
+    wg, wc = torch.empty(E, device="cuda"), torch.empty(E, f, d // 2, dtype=U8, device="cuda")
+    wsc = torch.empty(E, f, d // 16, dtype=U8, device="cuda")
+    M.moe_tensor_scale_microscaled(w, wg)
+    M.moe_quantize_microscaled(NV, w, wg, wc, wsc)
+    xg, xc = torch.empty(1, device="cuda"), torch.empty(P, d // 2, dtype=U8, device="cuda")
+    xs = torch.empty(P, d // 16, dtype=U8, device="cuda")
+    y = torch.zeros(P, f, dtype=BF, device="cuda")
+    sh = M.grouped_shape(P, E, f, d)
+    ws, lws = M.grouped_workspace(sh), M.workspace(cfg)
+
+    def go():
+        M.moe_dispatch(cfg, idx, x, off, perm, inv, gs, xp, lws)
+        M.moe_grouped_tensor_scale_microscaled(sh, xp, gs, off, xg, ws)
+        M.moe_quantize_microscaled(NV, xp, xg, xc, xs)
+        M.moe_grouped_gemm_microscaled(sh, NV, xc, xs, xg, gs, off, wc, wsc, wg, y, ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    want = None
+    for left in (0.0, 1e30, float("nan"), float("inf"), 3.0):
+        xp.fill_(left)
+        y.zero_()
+        graph.replay()
+        assert M.moe_get_device_status(ws) == 0 and M.moe_get_device_status(lws) == 0
+        assert torch.equal(xg, tensor_scale(x.float().abs().max().reshape(1)))
+        want = y.clone() if want is None else want
+        assert torch.equal(y, want) and y[inv.long()].abs().max() > 0
