@@ -145,13 +145,18 @@ def lib():
                 f"{LIB_PATH} is missing: build it with `python -m sparse_moe_transformer_route_b200.build`"
             )
         L = ctypes.CDLL(LIB_PATH)
+        rebuild = "rebuild with `python -m sparse_moe_transformer_route_b200.build`"
+        # the version first: an older library lacks entry points of this binding
+        version = L.moe_abi_version() if hasattr(L, "moe_abi_version") else None
+        if version != ABI_VERSION:
+            raise RuntimeError(f"{LIB_PATH} implements ABI {version}, this binding ABI {ABI_VERSION}: {rebuild}")
+        missing = [name for name in _SIGS if not hasattr(L, name)]
+        if missing:
+            raise RuntimeError(f"{LIB_PATH} lacks {', '.join(missing)}: {rebuild}")
         for name, (res, args) in _SIGS.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        if L.moe_abi_version() != ABI_VERSION:
-            raise RuntimeError(f"{LIB_PATH} implements ABI {L.moe_abi_version()}, this binding ABI {ABI_VERSION}: "
-                               "rebuild with `python -m sparse_moe_transformer_route_b200.build`")
         _lib = L
     return _lib
 
