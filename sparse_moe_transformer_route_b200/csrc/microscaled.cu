@@ -21,7 +21,9 @@
 // bf16 take 107 us, 117 with CTAs that stay and loop, 135 with one piece at a time. Small
 // tensors take one piece a thread, which reaches four times as many SMs. A block's
 // threads (1 to 4) find amax with shuffles. Quantisation goes from the end of a group to
-// its start: what the tensor scale's pass has just read is still in L2 there.
+// its start: of one group about as large as L2, what the tensor scale's pass has read last
+// is still there (128 MB: both passes 69.6 us, 70.7 from the start on; smaller groups and
+// many groups, which both passes take in the same order: no difference).
 #include "ragged.cuh"
 
 namespace moe {

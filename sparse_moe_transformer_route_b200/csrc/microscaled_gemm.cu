@@ -27,8 +27,10 @@
 // PAIR: a tile of 256 output columns on the two CTAs of a cluster, each with its 128 rows
 // of the weight and half of the tile's rows in shared memory and the scales of its own
 // 128 weight rows and of all the tile's rows; the leader issues cta_group::2 copies and
-// MMAs for both (131072 rows, 64 experts: 338 us with one CTA a tile, 283 on pairs, 266
-// with the accumulator's release relaxed and shorter tile lookups). What bounds it is the
+// MMAs for both (131072 rows, 64 experts: 338 us with one CTA a tile, 283 on pairs, 258
+// with the accumulator's release relaxed, shorter tile lookups and scales looked up in
+// shared memory; replayed graphs with a cold L2, in a loop of calls of some seconds 332 at
+// the power cap). What bounds it is the
 // operands' way into shared memory: 38 KB a stage whose MMAs take 512 cycles, five
 // stages in flight, about 2 us from a stage's release to its next use.
 // The scale warps arrive on the leader's barrier without a cluster-scope release: each

@@ -59,8 +59,9 @@ __device__ __forceinline__ void checked_group(const int32_t* group_start, const 
   *count = static_cast<int32_t>(c);
 }
 
-// Reads the layout (all threads of the CTA; it ends with a block barrier). cols: column tiles of a row tile. SORTED: the
-// experts come by falling row count (equal counts in order of e).
+// Reads the layout (all threads of the CTA; it ends with a block barrier). cols: column
+// tiles of a row tile. SORTED: the experts come by falling row count (equal counts in
+// order of e).
 template <int MOST, int UNIT, bool SORTED>
 __device__ __forceinline__ void load_groups(RaggedGroups* g, const int32_t* group_start, const int32_t* offsets, int E,
                                             int64_t rows, int cols, int32_t* status) {

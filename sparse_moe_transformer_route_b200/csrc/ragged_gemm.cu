@@ -29,7 +29,9 @@
 // What bounds it: few rows, the stream of weights (64 rows over 64 experts of 2048 x
 // 2048: 55 us, 92% of the measured HBM rate); many, the tensor cores (one expert of
 // 32768 rows 164 us, 1,680 TFLOP/s; 131072 rows over 64 experts: dgrad and wgrad,
-// which also writes 1 GB of fp32, 1.65 ms together; under a lasting load the power cap).
+// which also writes 1 GB of fp32, 1.65 ms together). These and the figures below are
+// replayed graphs with a cold L2; in a loop of calls of some seconds the power cap bounds
+// the large ones (32768 rows over 64 experts 274 us instead of 213, the gradients 2.0 ms).
 //
 // PAIR: a tile is 256 x BN on the two CTAs of a cluster (the SMs of one TPC), each with
 // its 128 rows of the M operand, half of the N operand and its 128 accumulator rows;
@@ -83,7 +85,10 @@ struct RCfg {
   // buffer (wgrad), the accumulator is handed over every SUM_BLOCKS stages (512
   // terms) and the parts are added in fp32 registers, rounded to nearest. dW over 8192
   // rows is then off by 4.8e-7 of its norm, 1.0e-6 with parts of 1024 and 9.1e-6 as one
-  // sum (an fp32 library product: 9.5e-7), for less than 1% of the time.
+  // sum (an fp32 library product: 9.5e-7), for less than 1% of the time. A bf16 result's
+  // one sum over the width is off by about 2e-6 of itself after 2048 terms, a thousandth of
+  // the rounding that follows; parts would cost it 1 to 4% (32768 rows over 64 experts
+  // 213 -> 219 us).
   static constexpr bool PARTS = O32 || W;
   static constexpr int SUM_BLOCKS = 8;
   static constexpr uint32_t IDESC0 = make_idesc(false, A_MN, B_MN, BM, 0);  // N is added by the tile
@@ -655,9 +660,12 @@ cudaError_t run_weights(const void* dy, const void* x, const RArgs& a, cudaStrea
 }  // namespace
 
 // The kind of tile that ends first: its turns over the SMs times a turn's stages. The host
-// knows the groups' sum only: it takes them as equal and two standard deviations of a
-// random split taller, so that most groups fit the tile that it picks. For 64 groups of
-// 2048 x 2048 the fastest kind is 32 rows at 1 a group, 64 at up to 32 (90 against 100 us
+// does not know the groups: it takes the buffer's rows as their sum, equal groups, and each
+// two standard deviations of a random split taller, so that most groups fit the tile that
+// it picks. A buffer that is mostly padding gets taller tiles than its groups need: 64 rows
+// over 64 experts of 2048 x 2048 in moe_dispatch's buffer of 8192 rows take 66.5 us, back
+// to back 62.4 (4-bit: 28.7 and 27.3). The times a stage were fitted to one width. For 64
+// groups of 2048 x 2048 the fastest kind is 32 rows at 1 a group, 64 at up to 32 (90 against 100 us
 // with 32 rows), 128 at 64 to 96 (96 against 139 and 100) and a pair from 128 on (102
 // against 106 with 256 rows); a single group of 96 rows takes 32 so that more SMs read
 // its weight.
